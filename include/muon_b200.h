@@ -319,6 +319,122 @@ muon_status adamw_step_scheduled(const adamw_group* groups, int n_groups,
                                  const muon_schedule_state* state, muon_stream_t stream);
 
 /*
+ * Operators that make the gradients the step reads (no counterpart on the
+ * optimizer pages, which start from a gradient): for the AdamW parameters,
+ * embedding tables and norm gains and biases; for the Muon parameters, hidden
+ * matrices whose input was kept as an 8-bit checkpoint.  They write fp32 or
+ * bf16 gradient buffers of the layout the step takes (dense row-major), either
+ * overwriting them or adding to what they hold (`accumulate` != 0, one
+ * rounding of old + new).  Sums are in fp32, in an order that depends on the
+ * shapes and ids alone: two calls on the same inputs give the same bits.
+ *
+ * Conventions above hold, and:
+ *   Activations  x, y, dy, dx, out, dout are device matrices of fp32 or bf16
+ *                rows, `pitch` elements apart (pitch >= columns; the elements
+ *                between are neither read nor written), each pointer aligned
+ *                to its element.  Where columns are a multiple of 8, pointers
+ *                16-byte aligned and rows 16-byte multiples apart, 16-byte
+ *                accesses are used; the results are the same bits.
+ *   Parameters   tables, gains, biases and gradients of matrices and tables
+ *                are dense and 16-byte aligned; dgain and dbias aligned to
+ *                their element.
+ *   Workspace    256-byte aligned, at least the bytes the *_workspace_size
+ *                function of the same arguments gives (0 on invalid ones);
+ *                scratch, no initialisation.  Calls that share one must be
+ *                ordered.
+ *   Aliasing     outputs overlap no input, but y may be x and dx may be dy or
+ *                x (same pointer, pitch and type).
+ *   Sizes        rows, n <= 2^30; vocab <= 2^30; widths <= 65536 (layer norm
+ *                16384, else MUON_ERR_UNSUPPORTED).  Zero rows are a valid
+ *                call: gradients are then zeros, or left as they are when
+ *                accumulating.
+ */
+
+/*
+ * out[t] <- scale * table[ids[t]], t < n.  ids: device int32 or int64
+ * (ids_bits 32 or 64).  An id outside [0, vocab) stands for no token (padding,
+ * e.g. -1): its row of out is zeros.  The product is rounded once.
+ */
+muon_status muon_embedding_forward(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim,
+                                   const void* ids, int32_t ids_bits, int64_t n, float scale,
+                                   void* out, int32_t out_dtype, int64_t out_pitch,
+                                   muon_stream_t stream);
+
+/*
+ * grad[v] <- (grad[v] +) scale * sum over t with ids[t] = v of dout[t], for
+ * every row v of the table; ids outside [0, vocab) contribute nothing.  The
+ * ids are sorted on the device (stable), and each row of grad is summed by
+ * ascending t in one place; runs of more than 128 equal ids are summed in
+ * chunks of 32 first.  With `accumulate`, rows whose id does not occur are
+ * neither read nor written.
+ */
+size_t muon_embedding_grad_workspace_size(int64_t vocab, int64_t dim, int64_t n);
+muon_status muon_embedding_grad(const void* dout, int32_t dout_dtype, int64_t dout_pitch,
+                                const void* ids, int32_t ids_bits, int64_t n, int64_t vocab,
+                                int64_t dim, float scale, void* grad, int32_t grad_dtype,
+                                int accumulate, void* workspace, size_t workspace_bytes,
+                                muon_stream_t stream);
+
+/*
+ * Layer norm of each row: mean = sum x / cols, rstd = 1 / sqrt(sum (x -
+ * mean)^2 / cols + eps), y <- (x - mean) * rstd * gain + bias.  gain: fp32
+ * [cols]; bias: fp32 [cols] or NULL (none).  mean, rstd: fp32 [rows], written
+ * for the backward pass.
+ */
+muon_status muon_layer_norm_forward(const void* x, int32_t x_dtype, int64_t x_pitch, int64_t rows,
+                                    int64_t cols, const float* gain, const float* bias, float eps,
+                                    void* y, int32_t y_dtype, int64_t y_pitch, float* mean,
+                                    float* rstd, muon_stream_t stream);
+
+/*
+ * With xh = (x - mean) * rstd and gy = dy * gain, per row:
+ *   dx <- rstd * (gy - mean(gy) - xh * mean(gy * xh))
+ * and over the rows: dgain <- (dgain +) sum dy * xh, dbias <- (dbias +) sum dy.
+ * dy, x and dx have one type (dtype); dgain and dbias one (grad_dtype); dbias
+ * may be NULL.
+ */
+size_t muon_layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
+muon_status muon_layer_norm_backward(const void* dy, int64_t dy_pitch, const void* x, int32_t dtype,
+                                     int64_t x_pitch, int64_t rows, int64_t cols, const float* gain,
+                                     const float* mean, const float* rstd, void* dx, int64_t dx_pitch,
+                                     void* dgain, void* dbias, int32_t grad_dtype, int accumulate,
+                                     void* workspace, size_t workspace_bytes, muon_stream_t stream);
+
+/*
+ * A checkpoint of activations x [rows, cols] in 8 bits: codes [rows] rows of
+ * code_pitch bytes (>= cols, a multiple of 16; 16-byte aligned; bytes past
+ * cols hold zeros) and exponents [rows][ceil(cols / 128)] bytes.  Feature c of
+ * row t is  e4m3(codes[t][c]) * 2^(exponents[t][c / 128] - 127):  8-bit floats
+ * of 4 exponent and 3 mantissa bits, and per row and block of 128 features the
+ * smallest power of two (at least 2^-124) that brings the block's largest
+ * magnitude to at most 448 (127 for a block of zeros).  Codes are rounded to
+ * nearest even: an error of at most 2^-4 of the value, or 2^-10 times the
+ * power of two for the smallest.  A block with an infinity or NaN has exponent
+ * 255 and stands for NaN throughout.  Restored values are exact in bf16 and
+ * fp32 (values that round up past the type's largest become infinite).
+ */
+muon_status muon_checkpoint_pack(const void* x, int32_t x_dtype, int64_t x_pitch, int64_t rows,
+                                 int64_t cols, uint8_t* codes, int64_t code_pitch,
+                                 uint8_t* exponents, muon_stream_t stream);
+muon_status muon_checkpoint_unpack(const uint8_t* codes, int64_t code_pitch,
+                                   const uint8_t* exponents, int64_t rows, int64_t cols, void* out,
+                                   int32_t out_dtype, int64_t out_pitch, muon_stream_t stream);
+
+/*
+ * The gradient of a hidden matrix W [n, k] (y = x W^T) from a checkpoint of
+ * its input x [rows, k] and dy [rows, n]:
+ *   grad[i][j] <- (grad[i][j] +) sum over t of dy[t][i] * x[t][j]
+ * with x as the checkpoint holds it.
+ */
+size_t muon_checkpoint_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype);
+muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_t dy_pitch,
+                                        int64_t rows, int64_t n, const uint8_t* codes,
+                                        int64_t code_pitch, const uint8_t* exponents, int64_t k,
+                                        void* grad, int32_t grad_dtype, int accumulate,
+                                        void* workspace, size_t workspace_bytes,
+                                        muon_stream_t stream);
+
+/*
  * AdamW's failure channel (it takes no caller workspace).  Synchronises
  * `stream` and returns MUON_ERR_TIMEOUT if, since the previous call, a
  * bounded device wait inside an adamw_step / adamw_step_scheduled kernel on

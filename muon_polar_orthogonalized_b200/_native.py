@@ -78,6 +78,25 @@ SIGNATURES = {
     "adamw_step_scheduled": (c_int, [POINTER(AdamWGroup), c_int, c_void_p, c_void_p]),
     "muon_query_status": (c_int, [c_void_p, c_void_p]),
     "adamw_query_status": (c_int, [c_void_p]),
+    "muon_embedding_forward": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32, c_int64,
+                                       c_float, c_void_p, c_int32, c_int64, c_void_p]),
+    "muon_embedding_grad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64]),
+    "muon_embedding_grad": (c_int, [c_void_p, c_int32, c_int64, c_void_p, c_int32, c_int64, c_int64, c_int64,
+                                    c_float, c_void_p, c_int32, c_int, c_void_p, c_size_t, c_void_p]),
+    "muon_layer_norm_forward": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                        c_float, c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p]),
+    "muon_layer_norm_backward_workspace_size": (c_size_t, [c_int64, c_int64]),
+    "muon_layer_norm_backward": (c_int, [c_void_p, c_int64, c_void_p, c_int32, c_int64, c_int64, c_int64,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p,
+                                         c_int32, c_int, c_void_p, c_size_t, c_void_p]),
+    "muon_checkpoint_pack": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_int64,
+                                     c_void_p, c_void_p]),
+    "muon_checkpoint_unpack": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_int32,
+                                       c_int64, c_void_p]),
+    "muon_checkpoint_weight_grad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "muon_checkpoint_weight_grad": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_int64,
+                                            c_void_p, c_int64, c_void_p, c_int32, c_int, c_void_p, c_size_t,
+                                            c_void_p]),
     "muon_selftest_wait_timeout": (c_int, [c_void_p, ctypes.c_uint64, c_void_p]),
     "muon_status_string": (c_char_p, [c_int]),
     "muon_last_error": (c_char_p, []),

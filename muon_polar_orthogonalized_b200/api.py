@@ -295,6 +295,262 @@ def adamw_step_scheduled(groups: Sequence[AdamWSpec], schedule_state, stream=Non
     check(st, "adamw_step_scheduled")
 
 
+# ------------------------------------------- operators that make the gradients
+def _on_device(fn: str, tensors, stream):
+    """(device context, stream handle) of a call whose tensors must share one
+    CUDA device; the stream defaults to that device's current one."""
+    import torch
+    dev = None
+    for name, t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: {name} is not a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, the others on {dev}")
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError(f"{fn}: stream of {s.device}, tensors on {dev}")
+    return torch.cuda.device(dev), c_void_p(int(s.cuda_stream))
+
+
+def _dtype_code(fn: str, name: str, t) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return N.MUON_F32
+    if t.dtype == torch.bfloat16:
+        return N.MUON_BF16
+    raise ValueError(f"{fn}: {name} must be fp32 or bf16, got {t.dtype}")
+
+
+def _rows(fn: str, name: str, t, cols: Optional[int] = None, rows: Optional[int] = None):
+    """(rows, columns, pitch) of an activation tensor [..., columns]: rows of
+    adjacent elements a constant pitch apart."""
+    if t.dim() < 1:
+        raise ValueError(f"{fn}: {name} has no dimension")
+    c = t.shape[-1]
+    r = 1
+    for d in t.shape[:-1]:
+        r *= d
+    if (cols is not None and c != cols) or (rows is not None and r != rows):
+        raise ValueError(f"{fn}: {name} {tuple(t.shape)} is not {'*' if rows is None else rows} rows of "
+                         f"{'*' if cols is None else cols}")
+    if c > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{fn}: the elements of a row of {name} are not adjacent")
+    pitch, span = None, 1   # leading dimensions, innermost first, must step evenly through the rows
+    for size, stride in list(zip(t.shape[:-1], t.stride()[:-1]))[::-1]:
+        if size == 1:
+            continue
+        if pitch is None:
+            pitch = stride
+        elif stride != pitch * span:
+            raise ValueError(f"{fn}: the rows of {name} are not a constant pitch apart")
+        span *= size
+    if pitch is None or r == 0:
+        pitch = c
+    if pitch < c:
+        raise ValueError(f"{fn}: the rows of {name} overlap")
+    return r, c, pitch
+
+
+def _dense(fn: str, name: str, t, shape, dtype=None) -> None:
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{fn}: {name} must be a contiguous{'' if dtype is None else f' {dtype}'} tensor of shape "
+                         f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _ids(fn: str, ids):
+    import torch
+    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError(f"{fn}: ids must be a contiguous int32 or int64 tensor")
+    return (32 if ids.dtype == torch.int32 else 64), ids.numel()
+
+
+def _ptr(t) -> c_void_p:
+    return c_void_p(0 if t is None else t.data_ptr())
+
+
+def _workspace(fn: str, ws) -> int:
+    if not ws.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
+def muon_embedding_forward(table, ids, out, scale: float = 1.0, stream=None) -> None:
+    """out[t] <- scale * table[ids[t]]; zeros where ids[t] is outside
+    [0, vocab).  table: fp32 or bf16 [vocab, dim]; ids: int32 or int64, any
+    shape; out: fp32 or bf16 [*ids.shape, dim] (rows may be strided)."""
+    fn = "muon_embedding_forward"
+    ctx, s = _on_device(fn, (("table", table), ("ids", ids), ("out", out)), stream)
+    if table.dim() != 2:
+        raise ValueError(f"{fn}: table must be [vocab, dim]")
+    vocab, dim = table.shape
+    _dense(fn, "table", table, (vocab, dim))
+    bits, n = _ids(fn, ids)
+    _, _, pitch = _rows(fn, "out", out, dim, n)
+    with ctx:
+        st = N.lib().muon_embedding_forward(_ptr(table), _dtype_code(fn, "table", table), vocab, dim, _ptr(ids), bits,
+                                            n, float(scale), _ptr(out), _dtype_code(fn, "out", out), pitch, s)
+    check(st, fn)
+
+
+def muon_embedding_grad_workspace_size(vocab: int, dim: int, n: int) -> int:
+    return int(N.lib().muon_embedding_grad_workspace_size(int(vocab), int(dim), int(n)))
+
+
+def muon_embedding_grad(dout, ids, grad, workspace, scale: float = 1.0, accumulate: bool = False,
+                        stream=None) -> None:
+    """grad[v] <- (grad[v] +) scale * sum of dout[t] over t with ids[t] = v.
+    dout: fp32 or bf16 [*ids.shape, dim]; grad: fp32 or bf16 [vocab, dim]."""
+    fn = "muon_embedding_grad"
+    ctx, s = _on_device(fn, (("dout", dout), ("ids", ids), ("grad", grad), ("workspace", workspace)), stream)
+    if grad.dim() != 2:
+        raise ValueError(f"{fn}: grad must be [vocab, dim]")
+    vocab, dim = grad.shape
+    _dense(fn, "grad", grad, (vocab, dim))
+    bits, n = _ids(fn, ids)
+    _, _, pitch = _rows(fn, "dout", dout, dim, n)
+    with ctx:
+        st = N.lib().muon_embedding_grad(_ptr(dout), _dtype_code(fn, "dout", dout), pitch, _ptr(ids), bits, n, vocab,
+                                         dim, float(scale), _ptr(grad), _dtype_code(fn, "grad", grad),
+                                         1 if accumulate else 0, _ptr(workspace), _workspace(fn, workspace), s)
+    check(st, fn)
+
+
+def muon_layer_norm_forward(x, gain, bias, y, mean, rstd, eps: float = 1e-5, stream=None) -> None:
+    """y <- (x - mean) * rstd * gain + bias over the last dimension; mean and
+    rstd (fp32, one per row) are written for the backward pass.  x, y: fp32 or
+    bf16; gain, bias: fp32 [cols] (bias may be None)."""
+    import torch
+    fn = "muon_layer_norm_forward"
+    ctx, s = _on_device(fn, (("x", x), ("gain", gain), ("bias", bias), ("y", y), ("mean", mean), ("rstd", rstd)),
+                        stream)
+    rows, cols, xp = _rows(fn, "x", x)
+    _, _, yp = _rows(fn, "y", y, cols, rows)
+    _dense(fn, "gain", gain, (cols,), torch.float32)
+    if bias is not None:
+        _dense(fn, "bias", bias, (cols,), torch.float32)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _dense(fn, name, t.view(-1) if t.is_contiguous() else t, (rows,), torch.float32)
+    with ctx:
+        st = N.lib().muon_layer_norm_forward(_ptr(x), _dtype_code(fn, "x", x), xp, rows, cols, _ptr(gain), _ptr(bias),
+                                             float(eps), _ptr(y), _dtype_code(fn, "y", y), yp, _ptr(mean), _ptr(rstd),
+                                             s)
+    check(st, fn)
+
+
+def muon_layer_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(N.lib().muon_layer_norm_backward_workspace_size(int(rows), int(cols)))
+
+
+def muon_layer_norm_backward(dy, x, gain, mean, rstd, dx, dgain, dbias, workspace, accumulate: bool = False,
+                             stream=None) -> None:
+    """The gradients of muon_layer_norm_forward: dx (the type of x and dy),
+    and dgain and dbias (fp32 or bf16 [cols]; dbias may be None), overwritten
+    or added to."""
+    import torch
+    fn = "muon_layer_norm_backward"
+    ctx, s = _on_device(fn, (("dy", dy), ("x", x), ("gain", gain), ("mean", mean), ("rstd", rstd), ("dx", dx),
+                             ("dgain", dgain), ("dbias", dbias), ("workspace", workspace)), stream)
+    rows, cols, xp = _rows(fn, "x", x)
+    _, _, dyp = _rows(fn, "dy", dy, cols, rows)
+    _, _, dxp = _rows(fn, "dx", dx, cols, rows)
+    if not (dy.dtype == x.dtype == dx.dtype):
+        raise ValueError(f"{fn}: dy, x and dx must have one type, got {dy.dtype}, {x.dtype}, {dx.dtype}")
+    _dense(fn, "gain", gain, (cols,), torch.float32)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _dense(fn, name, t.view(-1) if t.is_contiguous() else t, (rows,), torch.float32)
+    _dense(fn, "dgain", dgain, (cols,))
+    if dbias is not None:
+        _dense(fn, "dbias", dbias, (cols,), dgain.dtype)
+    with ctx:
+        st = N.lib().muon_layer_norm_backward(_ptr(dy), dyp, _ptr(x), _dtype_code(fn, "x", x), xp, rows, cols,
+                                              _ptr(gain), _ptr(mean), _ptr(rstd), _ptr(dx), dxp, _ptr(dgain),
+                                              _ptr(dbias), _dtype_code(fn, "dgain", dgain), 1 if accumulate else 0,
+                                              _ptr(workspace), _workspace(fn, workspace), s)
+    check(st, fn)
+
+
+CHECKPOINT_BLOCK = 128   # features that share one exponent of a checkpoint
+
+
+class Checkpoint:
+    """Activations [rows, cols] kept in 8 bits: codes, uint8 [rows, pitch]
+    (8-bit floats, 4 exponent and 3 mantissa bits; pitch a multiple of 16, at
+    least cols), and exponents, uint8 [rows, ceil(cols / 128)]."""
+
+    def __init__(self, codes, exponents, cols: int):
+        import torch
+        nb = (int(cols) + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
+        if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.shape[1] < cols \
+                or codes.shape[1] % 16 != 0 or cols < 1:
+            raise ValueError("Checkpoint: codes must be contiguous uint8 [rows, pitch], pitch a multiple of 16 and "
+                             f"at least cols = {cols}, got {codes.dtype} {tuple(codes.shape)}")
+        _dense("Checkpoint", "exponents", exponents, (codes.shape[0], nb), torch.uint8)
+        self.codes, self.exponents, self.cols = codes, exponents, int(cols)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+def new_checkpoint(rows: int, cols: int, device) -> Checkpoint:
+    """An uninitialised checkpoint for muon_checkpoint_pack to fill."""
+    import torch
+    pitch = (int(cols) + 15) // 16 * 16
+    nb = (int(cols) + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
+    return Checkpoint(torch.empty(int(rows), pitch, dtype=torch.uint8, device=device),
+                      torch.empty(int(rows), nb, dtype=torch.uint8, device=device), cols)
+
+
+def muon_checkpoint_pack(x, ckpt: Checkpoint, stream=None) -> None:
+    """Fill ckpt from x, fp32 or bf16 [..., cols] (rows may be strided)."""
+    fn = "muon_checkpoint_pack"
+    ctx, s = _on_device(fn, (("x", x), ("codes", ckpt.codes), ("exponents", ckpt.exponents)), stream)
+    rows, cols, pitch = _rows(fn, "x", x, ckpt.cols, ckpt.rows)
+    with ctx:
+        st = N.lib().muon_checkpoint_pack(_ptr(x), _dtype_code(fn, "x", x), pitch, rows, cols, _ptr(ckpt.codes),
+                                          ckpt.codes.shape[1], _ptr(ckpt.exponents), s)
+    check(st, fn)
+
+
+def muon_checkpoint_unpack(ckpt: Checkpoint, out, stream=None) -> None:
+    """out <- the values the checkpoint stands for (fp32 or bf16, both exact)."""
+    fn = "muon_checkpoint_unpack"
+    ctx, s = _on_device(fn, (("codes", ckpt.codes), ("exponents", ckpt.exponents), ("out", out)), stream)
+    rows, cols, pitch = _rows(fn, "out", out, ckpt.cols, ckpt.rows)
+    with ctx:
+        st = N.lib().muon_checkpoint_unpack(_ptr(ckpt.codes), ckpt.codes.shape[1], _ptr(ckpt.exponents), rows, cols,
+                                            _ptr(out), _dtype_code(fn, "out", out), pitch, s)
+    check(st, fn)
+
+
+def muon_checkpoint_weight_grad_workspace_size(rows: int, n: int, k: int, dy_dtype) -> int:
+    """dy_dtype: torch.float32 or torch.bfloat16."""
+    import torch
+    code = {torch.float32: N.MUON_F32, torch.bfloat16: N.MUON_BF16}.get(dy_dtype, -1)
+    return int(N.lib().muon_checkpoint_weight_grad_workspace_size(int(rows), int(n), int(k), code))
+
+
+def muon_checkpoint_weight_grad(dy, ckpt: Checkpoint, grad, workspace, accumulate: bool = False,
+                                stream=None) -> None:
+    """grad [n, k] <- (grad +) dy^T x: the gradient of W [n, k] in y = x W^T from
+    dy (fp32 or bf16 [..., n]) and the checkpoint of x [rows, k]."""
+    fn = "muon_checkpoint_weight_grad"
+    ctx, s = _on_device(fn, (("dy", dy), ("codes", ckpt.codes), ("exponents", ckpt.exponents), ("grad", grad),
+                             ("workspace", workspace)), stream)
+    rows, n, pitch = _rows(fn, "dy", dy, None, ckpt.rows)
+    _dense(fn, "grad", grad, (n, ckpt.cols))
+    with ctx:
+        st = N.lib().muon_checkpoint_weight_grad(_ptr(dy), _dtype_code(fn, "dy", dy), pitch, rows, n,
+                                                 _ptr(ckpt.codes), ckpt.codes.shape[1], _ptr(ckpt.exponents),
+                                                 ckpt.cols, _ptr(grad), _dtype_code(fn, "grad", grad),
+                                                 1 if accumulate else 0, _ptr(workspace), _workspace(fn, workspace), s)
+    check(st, fn)
+
+
 def muon_query_status(workspace, stream=None) -> int:
     ws = workspace if isinstance(workspace, int) else workspace.data_ptr()
     return int(N.lib().muon_query_status(c_void_p(ws), c_void_p(_stream_handle(stream))))

@@ -1,0 +1,98 @@
+// grad_params.cuh -- parameter blocks of the operators that make the
+// optimizer's gradients, shared by their kernels and entry points.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace muon {
+
+// ------------------------------------------------------------ embedding
+struct EmbedParams {
+  const void* table;   // [vocab, dim]
+  const void* ids;     // [n] int32 or int64
+  void* out;           // [n, dim], row pitch out_ld elements
+  long long vocab, n, out_ld;
+  int dim;
+  int ids64, table_bf16, out_bf16;
+  int vec;             // 16-byte accesses allowed
+  float scale;
+};
+
+constexpr int kEmbedChunk = 32;        // sorted positions per chunk of a long run
+constexpr int kEmbedLongRun = 128;     // runs of one token longer than this are summed by chunks
+
+struct EmbedGradParams {
+  const void* dout;    // [n, dim], row pitch dout_ld elements
+  const void* ids;
+  void* grad;          // [vocab, dim]
+  long long vocab, n, dout_ld;
+  int dim;
+  int ids64, dout_bf16, grad_bf16, accumulate;
+  int vec;
+  float scale;
+  // workspace
+  unsigned int* status;   // word 0: cleared by every call (muon_query_status)
+  uint32_t* keys[2];   // [n] sort buffers: ids (vocab for "no token") ...
+  uint32_t* pos[2];    // ... and the positions they come from
+  uint32_t* lo;        // [vocab] first and one past the last sorted position of each id
+  uint32_t* hi;
+  float* partial;      // [n / kEmbedChunk][dim] sums of whole chunks of long runs
+  int passes, bits;    // radix sort: passes of `bits` bits
+};
+
+// ------------------------------------------------------------ layer norm
+constexpr int kNormMaxCols = 16384;
+struct NormParams {
+  const void* x; const void* dy;
+  const float* gain; const float* bias;
+  void* y;             // forward: y; backward: dx
+  float* mean; float* rstd;
+  void* dgain; void* dbias;
+  float* partial;      // backward: [blocks][2][cols]
+  unsigned int* status;   // backward: workspace word 0
+  long long rows, x_ld, dy_ld, y_ld;
+  int cols;
+  int x_bf16, y_bf16, grad_bf16, accumulate;
+  int vec;
+  int blocks;          // backward: persistent blocks
+  float eps;
+};
+
+// ------------------------------------------------------------ checkpoints
+constexpr int kCkptBlock = 128;        // features sharing one exponent
+struct CkptParams {
+  const void* x;       // pack: source; unpack: unused
+  void* out;           // unpack: destination
+  uint8_t* q;          // [rows][q_ld] e4m3 codes
+  uint8_t* exps;       // [rows][nblk] exponents (power of two = e - 127; 255: NaN)
+  long long rows, x_ld, out_ld, q_ld;
+  int cols, nblk;
+  int bf16;            // type of x / out
+  int vec;
+};
+
+struct WeightGradParams {
+  const void* dy;      // [rows, n], row pitch dy_ld elements
+  const uint8_t* q; const uint8_t* exps;
+  void* grad;          // [n, k]
+  unsigned int* status;   // workspace word 0
+  long long rows, dy_ld, q_ld;
+  int n, k, nblk;
+  int dy_bf16, grad_bf16, accumulate;
+};
+
+cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s);
+cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s);
+cudaError_t launch_embedding_chunks(const EmbedGradParams& p, cudaStream_t s);
+cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s);
+cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s);
+cudaError_t launch_layer_norm_grad(const NormParams& p, cudaStream_t s);
+cudaError_t launch_layer_norm_columns(const NormParams& p, cudaStream_t s);
+int layer_norm_grad_blocks(long long rows, int cols, int sms);
+cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s);
+cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s);
+cudaError_t launch_weight_grad(const WeightGradParams& p, cudaStream_t s);
+
+}  // namespace muon

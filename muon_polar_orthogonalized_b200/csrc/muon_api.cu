@@ -22,6 +22,7 @@
 #include "../../include/muon_b200.h"
 #include "common.cuh"
 #include "elt_params.cuh"
+#include "host_api.cuh"
 
 namespace muon {
 // kernels (k_elementwise.cu, k_gemm_tc.cu, k_gemm_simt.cu)
@@ -75,14 +76,11 @@ void muon_set_last_error(const char* msg) { snprintf(g_err, sizeof(g_err), "%s",
 
 // ============================================================== profiler
 namespace {
-enum Kind {
-  K_MOMENTUM = 0, K_NORM, K_GRAM, K_POLY, K_AXPY, K_AXPY_UPDATE, K_UPDATE, K_EMIT, K_ADAMW,
-  K_GRAM_F32, K_POLY_F32, K_AXPY_F32, K_AXPY_UPDATE_F32, K_NORMUON_UPDATE, K_MOMENTUM_ROWEQ, K_COUNT
-};
 const char* const kKindNames[K_COUNT] = {
     "momentum_norm", "norm_finalize", "ns_gram", "ns_poly", "ns_axpy", "ns_axpy_update",
     "update", "emit", "adamw", "ns_gram_f32", "ns_poly_f32", "ns_axpy_f32", "ns_axpy_update_f32",
-    "normuon_update", "momentum_rowq"};
+    "normuon_update", "momentum_rowq", "embedding", "embedding_sort", "embedding_grad", "layer_norm",
+    "layer_norm_grad", "checkpoint_pack", "checkpoint_unpack", "weight_grad"};
 
 struct ProfRec {
   int kind;
@@ -181,6 +179,41 @@ muon_status device_info(DevInfo* out) {
   return MUON_OK;
 }
 }  // namespace
+
+// What the other translation units with entry points use (host_api.cuh).
+namespace muon {
+void api_clear_error() { g_err[0] = '\0'; }
+muon_status api_fail(muon_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+muon_status api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+muon_status api_device(int* sms) {
+  DevInfo d;
+  const muon_status st = device_info(&d);
+  if (st == MUON_OK) *sms = d.sms;
+  return st;
+}
+cudaError_t api_timed_launch(int kind, cudaStream_t s, const std::function<cudaError_t()>& f) {
+  return timed_launch(kind, s, f);
+}
+muon_status api_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, void* base,
+                           const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                           CUtensorMapSwizzle swizzle) {
+  PFN_encodeTiled_t enc = get_encode();
+  if (!enc) return fail(MUON_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(map, type, static_cast<cuuint32_t>(rank), base, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return MUON_OK;
+}
+}  // namespace muon
 
 // ================================================================ planner
 namespace {
