@@ -424,9 +424,16 @@ muon_status muon_checkpoint_unpack(const uint8_t* codes, int64_t code_pitch,
  * The gradient of a hidden matrix W [n, k] (y = x W^T) from a checkpoint of
  * its input x [rows, k] and dy [rows, n]:
  *   grad[i][j] <- (grad[i][j] +) sum over t of dy[t][i] * x[t][j]
- * with x as the checkpoint holds it.
+ * with x as the checkpoint holds it, on the bf16 tensor cores with fp32 sums
+ * (their additions may drop the bits below a step).  No operand is rounded:
+ * fp32 dy is taken in three bf16 parts, at three times the work.
+ * dy is read in place where it is bf16, its pointer 16-byte aligned and its
+ * rows a multiple of 16 bytes apart and of 8 elements long; else it is copied
+ * into the workspace first.  dy_aligned says whether it will be (0 asks for
+ * the copy's bytes too; fp32 and n not a multiple of 8 imply it).
  */
-size_t muon_checkpoint_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype);
+size_t muon_checkpoint_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype,
+                                                  int dy_aligned);
 muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_t dy_pitch,
                                         int64_t rows, int64_t n, const uint8_t* codes,
                                         int64_t code_pitch, const uint8_t* exponents, int64_t k,

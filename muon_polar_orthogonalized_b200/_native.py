@@ -93,7 +93,7 @@ SIGNATURES = {
                                      c_void_p, c_void_p]),
     "muon_checkpoint_unpack": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_int32,
                                        c_int64, c_void_p]),
-    "muon_checkpoint_weight_grad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "muon_checkpoint_weight_grad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int]),
     "muon_checkpoint_weight_grad": (c_int, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_int64,
                                             c_void_p, c_int64, c_void_p, c_int32, c_int, c_void_p, c_size_t,
                                             c_void_p]),

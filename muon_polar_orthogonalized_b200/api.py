@@ -527,11 +527,14 @@ def muon_checkpoint_unpack(ckpt: Checkpoint, out, stream=None) -> None:
     check(st, fn)
 
 
-def muon_checkpoint_weight_grad_workspace_size(rows: int, n: int, k: int, dy_dtype) -> int:
-    """dy_dtype: torch.float32 or torch.bfloat16."""
+def muon_checkpoint_weight_grad_workspace_size(rows: int, n: int, k: int, dy_dtype, dy_aligned: bool = True) -> int:
+    """dy_dtype: torch.float32 or torch.bfloat16.  dy_aligned=False also counts
+    the copy of a bf16 dy whose pointer or row pitch is not a multiple of 16
+    bytes."""
     import torch
     code = {torch.float32: N.MUON_F32, torch.bfloat16: N.MUON_BF16}.get(dy_dtype, -1)
-    return int(N.lib().muon_checkpoint_weight_grad_workspace_size(int(rows), int(n), int(k), code))
+    return int(N.lib().muon_checkpoint_weight_grad_workspace_size(int(rows), int(n), int(k), code,
+                                                                   1 if dy_aligned else 0))
 
 
 def muon_checkpoint_weight_grad(dy, ckpt: Checkpoint, grad, workspace, accumulate: bool = False,

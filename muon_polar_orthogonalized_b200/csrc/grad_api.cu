@@ -109,6 +109,41 @@ muon_status check_checkpoint(const void* q, int64_t q_ld, const void* exps, int6
     return api_fail(MUON_ERR_INVALID_ARG, "codes or exponents: NULL, or codes not 16-byte aligned");
   return MUON_OK;
 }
+
+// Plan of a weight gradient: staging of dy and the split of its rows.
+struct WeightWs {
+  int planes;      // bf16 planes dy is staged in (0: read as it is)
+  int64_t pitch;   // of a staged row
+  int kblocks, splits;
+  size_t staged, total;
+};
+WeightWs weight_ws(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype, bool dy_aligned) {
+  WeightWs w = {};
+  w.planes = dy_dtype == MUON_F32 ? 3 : dy_aligned ? 0 : 1;
+  w.pitch = (n + 63) / 64 * 64;
+  w.staged = up256(static_cast<size_t>(w.planes) * rows * w.pitch * 2);
+  const int64_t kb = (rows + 63) / 64 * std::max(w.planes, 1);
+  w.kblocks = static_cast<int>(kb);
+  // Split the rows so that the units fill the CTA pairs: the estimated time of
+  // a wave is its stages plus a fixed cost, and splits above one cost their
+  // sums' write and read and another launch (in units of one stage, 0.3 us).
+  const int64_t tiles = ((n + 255) / 256) * ((k + 255) / 256);
+  const int pairs = 74;
+  double best = 1e300;
+  w.splits = 1;
+  for (int64_t sp = 1; sp <= std::min<int64_t>(kb, 32); ++sp) {
+    if (sp > 1 && tiles * sp > 2 * pairs) break;
+    const double waves = static_cast<double>((tiles * sp + pairs - 1) / pairs);
+    const double join = sp == 1 ? 0.0 : 8.0 + static_cast<double>(sp) * n * k * 8.0 / (4e6 * 0.3);
+    const double cost = waves * (static_cast<double>((kb + sp - 1) / sp) + 10.0) + join;
+    if (cost < best) {
+      best = cost;
+      w.splits = static_cast<int>(sp);
+    }
+  }
+  w.total = 256 + w.staged + (w.splits > 1 ? up256(static_cast<size_t>(w.splits) * n * k * 4) : 0);
+  return w;
+}
 }  // namespace
 
 extern "C" {
@@ -353,9 +388,10 @@ muon_status muon_checkpoint_unpack(const uint8_t* codes, int64_t code_pitch, con
   });
 }
 
-size_t muon_checkpoint_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype) {
+size_t muon_checkpoint_weight_grad_workspace_size(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype,
+                                                  int dy_aligned) {
   if (rows < 0 || rows > kMaxRows || n < 1 || n > kMaxDim || k < 1 || k > kMaxDim || !is_dtype(dy_dtype)) return 0;
-  return 256;
+  return weight_ws(rows, n, k, dy_dtype, dy_aligned && n % 8 == 0).total;
 }
 
 muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_t dy_pitch, int64_t rows, int64_t n,
@@ -369,30 +405,79 @@ muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_
     if ((st = check_rows("dy", dy, dy_dtype, rows, n, dy_pitch)) != MUON_OK) return st;
     if (!is_dtype(grad_dtype)) return api_fail(MUON_ERR_INVALID_ARG, "grad: dtype %d unknown", grad_dtype);
     if (!grad || !aligned_to(grad, 16)) return api_fail(MUON_ERR_INVALID_ARG, "grad: NULL or not 16-byte aligned");
-    if ((st = check_workspace(workspace, workspace_bytes,
-                              muon_checkpoint_weight_grad_workspace_size(rows, n, k, dy_dtype))) != MUON_OK)
-      return st;
+    const WeightWs w = weight_ws(rows, n, k, dy_dtype, rows_vec(dy, dy_dtype, n, dy_pitch));
+    if ((st = check_workspace(workspace, workspace_bytes, w.total)) != MUON_OK) return st;
     int sms;
     if ((st = api_device(&sms)) != MUON_OK) return st;
-    if (rows == 0 && accumulate) return MUON_OK;
-    WeightGradParams p = {};
-    p.dy = dy;
-    p.q = codes;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+      if (!accumulate)
+        st = launched(cudaMemsetAsync(grad, 0, static_cast<size_t>(n) * k * elem(grad_dtype), s), "zero gradient");
+      if (st == MUON_OK) st = launched(cudaMemsetAsync(workspace, 0, 4, s), "clear status");
+      return st;
+    }
+    WeightGradTc p = {};
+    char* base = static_cast<char*>(workspace);
+    const void* src = dy;
+    int64_t ld = dy_pitch;
+    if (w.planes > 0) {   // staged as bf16
+      src = base + 256;
+      ld = w.pitch;
+      st = launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] {
+                      return launch_weight_grad_stage(dy, dy_dtype == MUON_BF16, dy_pitch, base + 256, rows,
+                                                      static_cast<int>(n), static_cast<int>(w.pitch), s);
+                    }), "weight gradient staging launch");
+      if (st != MUON_OK) return st;
+    }
+    const int planes = std::max(w.planes, 1);
+    const cuuint64_t R = static_cast<cuuint64_t>(rows), row_bytes = static_cast<cuuint64_t>(ld) * 2;
+    const cuuint64_t plane_bytes = planes > 1 ? row_bytes * R : row_bytes;   // one plane: never stepped
+    // 64-column chunks as a dimension of their own where rows are whole chunks
+    const int64_t width = w.planes > 0 ? w.pitch : n;
+    p.chunked = width % 64 == 0;
+    if (p.chunked) {
+      const cuuint64_t dims[4] = {64, R, static_cast<cuuint64_t>(width / 64), static_cast<cuuint64_t>(planes)};
+      const cuuint64_t strides[3] = {row_bytes, 128, plane_bytes};
+      const cuuint32_t box[4] = {64, 64, 2, 1};
+      st = api_tensor_map(&p.tm_dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(src), dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+      const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), R, static_cast<cuuint64_t>(planes)};
+      const cuuint64_t strides[2] = {row_bytes, plane_bytes};
+      const cuuint32_t box[3] = {64, 64, 1};
+      st = api_tensor_map(&p.tm_dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(src), dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (st != MUON_OK) return st;
+    {
+      const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), R, 1};
+      const cuuint64_t strides[2] = {static_cast<cuuint64_t>(code_pitch), static_cast<cuuint64_t>(code_pitch)};
+      const cuuint32_t box[3] = {128, 64, 1};
+      st = api_tensor_map(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_NONE);
+      if (st != MUON_OK) return st;
+    }
     p.exps = exponents;
     p.grad = grad;
     p.status = static_cast<unsigned int*>(workspace);
+    p.partial = reinterpret_cast<float*>(base + 256 + w.staged);
     p.rows = rows;
-    p.dy_ld = dy_pitch;
-    p.q_ld = code_pitch;
     p.n = static_cast<int>(n);
     p.k = static_cast<int>(k);
     p.nblk = (p.k + kCkptBlock - 1) / kCkptBlock;
-    p.dy_bf16 = dy_dtype == MUON_BF16;
+    p.row_blocks = static_cast<int>((rows + 63) / 64);
+    p.kblocks = w.kblocks;
+    p.tiles_n = (p.n + 255) / 256;
+    p.tiles_k = (p.k + 255) / 256;
+    p.splits = w.splits;
+    p.units = p.tiles_n * p.tiles_k * p.splits;
     p.grad_bf16 = grad_dtype == MUON_BF16;
     p.accumulate = accumulate != 0;
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad(p, s); }),
-                    "weight gradient launch");
+    st = launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad_tc(p, sms, s); }),
+                  "weight gradient launch");
+    if (st != MUON_OK || p.splits == 1) return st;
+    return launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad_join(p, s); }),
+                    "weight gradient join launch");
   });
 }
 

@@ -73,14 +73,21 @@ struct CkptParams {
   int vec;
 };
 
-struct WeightGradParams {
-  const void* dy;      // [rows, n], row pitch dy_ld elements
-  const uint8_t* q; const uint8_t* exps;
+// The weight gradient on the tensor cores (k_weight_grad.cu).
+struct alignas(64) WeightGradTc {
+  CUtensorMap tm_dy;   // bf16 dy: (n, rows, planes), or (64, rows, n / 64, planes) when chunked
+  CUtensorMap tm_q;    // codes: (k, rows, 1)
+  const uint8_t* exps;
   void* grad;          // [n, k]
+  float* partial;      // splits > 1: [splits][n][k]
   unsigned int* status;   // workspace word 0
-  long long rows, dy_ld, q_ld;
+  long long rows;
   int n, k, nblk;
-  int dy_bf16, grad_bf16, accumulate;
+  int chunked;
+  int row_blocks;      // 64-row blocks of one plane
+  int kblocks;         // planes * row_blocks
+  int tiles_n, tiles_k, splits, units;
+  int grad_bf16, accumulate;
 };
 
 cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s);
@@ -93,6 +100,9 @@ cudaError_t launch_layer_norm_columns(const NormParams& p, cudaStream_t s);
 int layer_norm_grad_blocks(long long rows, int cols, int sms);
 cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s);
 cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s);
-cudaError_t launch_weight_grad(const WeightGradParams& p, cudaStream_t s);
+cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,
+                                     int pitch, cudaStream_t s);
+cudaError_t launch_weight_grad_tc(const WeightGradTc& p, int sms, cudaStream_t s);
+cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s);
 
 }  // namespace muon

@@ -12,7 +12,7 @@
 //
 //   pack         x -> codes, exponents     reads x once, writes cols + cols/128 bytes per row
 //   unpack       the reverse
-//   weight_grad  dW[n][k] (+)= sum over rows t of dy[t][n] * value[t][k]
+// The weight gradient from a checkpoint is in k_weight_grad.cu.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -121,50 +121,6 @@ __global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_kernel(const Ckp
   }
 }
 
-// ------------------------------------------------------- weight gradient
-constexpr int kWgTile = 64, kWgDepth = 16;
-template <typename D, typename G>
-__global__ void __launch_bounds__(256) weight_grad_kernel(const WeightGradParams p) {
-  __shared__ float a[kWgDepth][kWgTile + 4], b[kWgDepth][kWgTile + 4];
-  pdl_launch_dependents();
-  pdl_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
-  const int n0 = blockIdx.y * kWgTile, k0 = blockIdx.x * kWgTile;
-  const int tn = (threadIdx.x / 16) * 4, tk = (threadIdx.x % 16) * 4;
-  float acc[4][4] = {};
-  for (long long t0 = 0; t0 < p.rows; t0 += kWgDepth) {
-    for (int i = threadIdx.x; i < kWgDepth * kWgTile; i += 256) {
-      const int r = i / kWgTile, c = i % kWgTile;
-      const long long t = t0 + r;
-      float va = 0.f, vb = 0.f;
-      if (t < p.rows && n0 + c < p.n) va = to_f32(static_cast<const D*>(p.dy)[t * p.dy_ld + n0 + c]);
-      if (t < p.rows && k0 + c < p.k)
-        vb = codes2(p.q[t * p.q_ld + k0 + c]).x * block_factor(p.exps[t * p.nblk + (k0 + c) / kCkptBlock]);
-      a[r][c] = va;
-      b[r][c] = vb;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kWgDepth; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[r][tn + i], b[r][tk + j], acc[i][j]);
-    __syncthreads();
-  }
-  G* out = static_cast<G*>(p.grad);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tn + i, k = k0 + tk + j;
-      if (n < p.n && k < p.k) {
-        G* o = out + static_cast<long long>(n) * p.k + k;
-        *o = from_f32<G>(acc[i][j] + (p.accumulate ? to_f32(*o) : 0.f));
-      }
-    }
-}
-
 // ---------------------------------------------------------------- launchers
 static int ck_segments(long long cols) { return static_cast<int>((cols + 255) / 256); }
 static dim3 ck_grid(long long tasks) { return dim3(static_cast<unsigned>((tasks + kCkWarps - 1) / kCkWarps)); }
@@ -186,17 +142,6 @@ static cudaError_t unpack_typed(const CkptParams& p, cudaStream_t s) {
 cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s) {
   if (p.bf16) return p.vec ? unpack_typed<__nv_bfloat16, true>(p, s) : unpack_typed<__nv_bfloat16, false>(p, s);
   return p.vec ? unpack_typed<float, true>(p, s) : unpack_typed<float, false>(p, s);
-}
-
-template <typename D, typename G>
-static cudaError_t weight_typed(const WeightGradParams& p, cudaStream_t s) {
-  const dim3 grid((p.k + kWgTile - 1) / kWgTile, (p.n + kWgTile - 1) / kWgTile);
-  return launch_pdl(weight_grad_kernel<D, G>, grid, dim3(256), 0, s, p);
-}
-cudaError_t launch_weight_grad(const WeightGradParams& p, cudaStream_t s) {
-  using B = __nv_bfloat16;
-  if (p.dy_bf16) return p.grad_bf16 ? weight_typed<B, B>(p, s) : weight_typed<B, float>(p, s);
-  return p.grad_bf16 ? weight_typed<float, B>(p, s) : weight_typed<float, float>(p, s);
 }
 
 }  // namespace muon

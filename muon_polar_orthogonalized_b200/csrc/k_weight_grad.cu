@@ -1,0 +1,544 @@
+// k_weight_grad.cu -- a hidden matrix's gradient from an 8-bit checkpoint, on
+// the 5th-generation tensor cores.
+//
+//   dW[n][k] (+)= sum over rows t of dy[t][n] * x[t][k],
+//   x[t][k] = code[t][k] * 2^(e[t][k / 128] - 127)
+//
+// 2 T N K operations on operands of 2 T N + T K bytes: bound by the tensor
+// pipe for all but the smallest shapes.  The tensor cores' bf16 product needs
+// both operands in bf16, and every restored value is exact in bf16
+// (k_checkpoint.cu), so the codes are turned into bf16 on the way through
+// shared memory and never exist in memory at 2 bytes: the kernel reads half
+// the bytes of x that a product of kept bf16 activations would.
+//
+// Structure: persistent CTA pairs (cta_group::2) on 256 x 256 tiles of dW.
+// Both operands are MN-major (their rows are the summed index).  Per 64 rows
+// and stage, each CTA brings by TMA 128 columns of dy (bf16, 128-byte swizzle:
+// the MMA operand as it stands) and 128 columns of codes (exactly one exponent
+// per row), and eight warps write the codes' bf16 values into the second
+// operand's swizzled layout.  The leader issues 256x256x16 MMAs into one of
+// two 256-column accumulators, so that a tile's epilogue overlaps the next
+// tile's MMAs.
+//   warp 0: TMA producer      warp 1: MMA issuer (+ TMEM owner)
+//   warps 2-5: epilogue       warps 6-13: codes to bf16
+// Four instructions and a packed multiply turn two codes into two bf16: the
+// code's exponent and mantissa bits, moved to the low end of bf16's exponent
+// and the high end of its mantissa, read as the value times 2^-120 (bf16
+// subnormals and the code's line up), so one exact multiply by a power of two
+// finishes it.
+//
+// Few tiles, many rows: the rows are split over several units per tile, each
+// unit writes its fp32 sums to the workspace, and a second kernel adds them in
+// order.  dy in fp32, or with rows that TMA cannot read, is first staged in
+// the workspace as bf16: one plane for bf16, three for fp32 (each value is
+// the sum of its three parts to the last bit), which the product walks one
+// after another as if the rows repeated.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "grad_params.cuh"
+#include "pdl.cuh"
+#include "sm100.cuh"
+#include "vec8.cuh"
+
+namespace muon {
+
+namespace {
+constexpr int WG_BK = 64;                      // rows (summed index) per stage
+constexpr int WG_STAGES = 5;
+constexpr int WG_A_BYTES = 128 * WG_BK * 2;    // dy: two 64-column chunks
+constexpr int WG_B_BYTES = 128 * WG_BK * 2;    // restored x, likewise
+constexpr int WG_Q_BYTES = 128 * WG_BK;        // codes
+constexpr int WG_CHUNK = WG_BK * 128;          // one 64-column chunk of an operand
+constexpr int WG_STAGE = WG_A_BYTES + WG_B_BYTES + WG_Q_BYTES;
+constexpr int WG_EPI_WARPS = 4, WG_CVT_WARPS = 8;
+constexpr int WG_THREADS = 32 * (2 + WG_EPI_WARPS + WG_CVT_WARPS);
+constexpr int WG_BAR_OFF = WG_STAGES * WG_STAGE;
+constexpr int WG_SMEM = WG_BAR_OFF + 1024 + 1024;
+constexpr int WG_TMEM = 512;
+constexpr int WG_BAND = 8;                     // tile columns per raster band
+static_assert(WG_SMEM <= 232448, "shared memory per block");
+static_assert(WG_STAGE % 1024 == 0 && WG_A_BYTES % 1024 == 0, "swizzle atoms");
+constexpr uint32_t kTimeout = 1u;              // status word bit (muon_query_status)
+}  // namespace
+
+struct WgUnit {
+  int n0, k0, split, kb0, kb1;
+};
+
+__device__ __forceinline__ WgUnit wg_unit(const WeightGradTc& p, int u) {
+  const int tiles = p.tiles_n * p.tiles_k;
+  const int split = u / tiles;
+  int r = u - split * tiles;
+  const int band_tiles = p.tiles_n * WG_BAND;
+  const int band = r / band_tiles;
+  r -= band * band_tiles;
+  const int width = min(WG_BAND, p.tiles_k - band * WG_BAND);
+  const int tn = r / width;
+  const int tk = band * WG_BAND + (r - tn * width);
+  return {tn * 256, tk * 256, split, static_cast<int>(static_cast<long long>(p.kblocks) * split / p.splits),
+          static_cast<int>(static_cast<long long>(p.kblocks) * (split + 1) / p.splits)};
+}
+
+// Two codes in bytes 1 and 3 of x, as two bf16 times 2^-120.
+__device__ __forceinline__ uint32_t code_bits(uint32_t x) { return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t f) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16 codes of one exponent -> 16 bf16 in two 16-byte units.
+__device__ __forceinline__ void restore16(const uint4& q, int e, uint4& lo, uint4& hi) {
+  // 2^(120 + e - 127) fits bf16 up to e = 134; beyond, a second factor follows
+  const int p = e == 255 ? 0 : min(e - 7, 127);
+  uint32_t f = e == 255 ? 0x7fffu : static_cast<uint32_t>(p + 127) << 7;
+  f |= f << 16;
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[2 * i] = mul_bf16x2(code_bits(__byte_perm(w[i], 0, 0x1404)), f);
+    r[2 * i + 1] = mul_bf16x2(code_bits(__byte_perm(w[i], 0, 0x3424)), f);
+  }
+  if (e > 134 && e != 255) {
+    uint32_t g = static_cast<uint32_t>(e - 134 + 127) << 7;
+    g |= g << 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = mul_bf16x2(r[i], g);
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// One row's 32 columns of the output (fp32 or bf16), with 32-byte, 16-byte or
+// single accesses as its address and the columns left allow.
+template <typename G>
+__device__ __forceinline__ void store_row32(G* dst, const float (&v)[32], int cols, bool accumulate) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(dst);
+  if (cols >= 32 && (a & 15) == 0) {
+    float o[32];
+    if (accumulate) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load8(dst + 8 * k, *reinterpret_cast<float(*)[8]>(&o[8 * k]));
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] += v[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = v[k];
+    }
+    uint4 u[sizeof(G) * 2];
+    if constexpr (sizeof(G) == 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * k + 2 * h], o[8 * k + 2 * h + 1]);
+          w[h] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        u[k] = make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                          __float_as_uint(o[4 * k + 3]));
+    }
+    constexpr int N = sizeof(G) * 2;   // 16-byte units
+    if ((a & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) sm100::st_global_v8(reinterpret_cast<uint4*>(dst) + 2 * k, u[2 * k], u[2 * k + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) reinterpret_cast<uint4*>(dst)[k] = u[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (k < cols) dst[k] = from_f32<G>(v[k] + (accumulate ? to_f32(dst[k]) : 0.f));
+  }
+}
+
+__device__ __forceinline__ void wg_timeout(unsigned int* status, volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(status, kTimeout);
+}
+
+template <typename G>
+__global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __grid_constant__ WeightGradTc p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + WG_BAR_OFF);   // leader's: both CTAs' dy
+  uint64_t* full_q = full_a + WG_STAGES;                               // this CTA's codes
+  uint64_t* ready = full_q + WG_STAGES;                                // leader's: both CTAs' restored x
+  uint64_t* empty = ready + WG_STAGES;
+  uint64_t* tfull = empty + WG_STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(sm100::cluster_ctarank());
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < WG_STAGES; ++s) {
+      sm100::mbar_init(&full_a[s], 1);
+      sm100::mbar_init(&full_q[s], 1);
+      sm100::mbar_init(&ready[s], 2 * WG_CVT_WARPS);
+      sm100::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      sm100::mbar_init(&tfull[b], 1);
+      sm100::mbar_init(&tempty[b], 2 * WG_EPI_WARPS);
+    }
+    *abort_flag = 0;
+    sm100::fence_mbar_init();
+    sm100::prefetch_tmap(&p.tm_dy);
+    sm100::prefetch_tmap(&p.tm_q);
+  }
+  if (warp == 1) {
+    sm100::tmem_alloc_pair(tmem_slot, WG_TMEM);
+    sm100::tmem_relinquish_pair();
+  }
+  sm100::tc_fence_before();
+  __syncwarp();
+  sm100::cluster_sync();
+  sm100::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  // a wait that gives up does so seconds after this
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_phase = 0;
+      bool ok = true;
+      for (int u = first; u < p.units && ok; u += step) {
+        const WgUnit w = wg_unit(p, u);
+        const int nrow = w.n0 + rank * 128, kcol = w.k0 + rank * 128;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+            wg_timeout(p.status, abort_flag);
+            ok = false;
+            break;
+          }
+          const int plane = kb / p.row_blocks;
+          const int t0 = (kb - plane * p.row_blocks) * WG_BK;
+          uint8_t* sa = smem + stage * WG_STAGE;
+          uint8_t* sq = sa + WG_A_BYTES + WG_B_BYTES;
+          if (rank == 0) sm100::mbar_arrive_expect_tx(&full_a[stage], 2 * WG_A_BYTES);
+          sm100::mbar_arrive_expect_tx(&full_q[stage], WG_Q_BYTES);
+          issued |= 1u << stage;
+          issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+          sm100::tma_load_3d(sq, &p.tm_q, &full_q[stage], kcol, t0, 0);
+          const uint32_t bar = sm100::mapa_shared(sm100::smem_u32(&full_a[stage]), 0);
+          if (p.chunked) {
+            sm100::tma_load_4d_pair(sa, &p.tm_dy, bar, 0, t0, nrow / 64, plane);
+          } else {
+            sm100::tma_load_3d_pair(sa, &p.tm_dy, bar, nrow, t0, plane);
+            sm100::tma_load_3d_pair(sa + WG_CHUNK, &p.tm_dy, bar, nrow + 64, t0, plane);
+          }
+          if (++stage == WG_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        // let every load issued into this CTA's shared memory land before exit
+        for (int s = 0; s < WG_STAGES; ++s) {
+          if (!((issued >> s) & 1u)) continue;
+          const uint64_t t = sm100::globaltimer();
+          while ((!sm100::mbar_try_wait(&full_q[s], (issued_phase >> s) & 1u) ||
+                  (rank == 0 && !sm100::mbar_try_wait(&full_a[s], (issued_phase >> s) & 1u))) &&
+                 sm100::globaltimer() - t < 100000000ull) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = sm100::make_idesc_bf16(256, 256, 1, 1);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = first; u < p.units && ok; u += step) {
+        const WgUnit w = wg_unit(p, u);
+        if (!sm100::mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
+          wg_timeout(p.status, abort_flag);
+          break;
+        }
+        sm100::tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!sm100::mbar_wait(&full_a[stage], phase, abort_flag) ||
+              !sm100::mbar_wait(&ready[stage], phase, abort_flag)) {
+            wg_timeout(p.status, abort_flag);
+            ok = false;
+            break;
+          }
+          sm100::tc_fence_after();
+          const uint32_t sa = sm100::smem_u32(smem + stage * WG_STAGE);
+          const uint64_t ad = sm100::make_sdesc(sa, WG_CHUNK, 1024);
+          const uint64_t bd = sm100::make_sdesc(sa + WG_A_BYTES, WG_CHUNK, 1024);
+#pragma unroll
+          for (int kk = 0; kk < WG_BK / 16; ++kk)
+            sm100::umma_bf16_pair(d, ad + static_cast<uint64_t>(kk * (2048 >> 4)),
+                                  bd + static_cast<uint64_t>(kk * (2048 >> 4)), idesc, (kb > w.kb0 || kk) ? 1u : 0u);
+          sm100::umma_commit_pair_both(&empty[stage]);
+          if (++stage == WG_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        sm100::umma_commit_pair_both(&tfull[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp < 2 + WG_EPI_WARPS) {
+    // ----------------------------------------------------------- epilogue
+    const int quad = warp & 3;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int u = first; u < p.units; u += step) {
+      const WgUnit w = wg_unit(p, u);
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&tfull[acc], acc_phase, abort_flag))) {
+        if (lane == 0) wg_timeout(p.status, abort_flag);
+        break;
+      }
+      sm100::tc_fence_after();
+      const int row = w.n0 + rank * 128 + quad * 32 + lane;
+      const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      const int nch = min(8, (p.k - w.k0 + 31) / 32);
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        uint32_t r[32];
+        sm100::tmem_ld32_async(t_row + static_cast<uint32_t>(c * 32), r);
+        sm100::tmem_wait_ld(r);
+        if (row < p.n) {
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+          const int j = w.k0 + c * 32;
+          if (p.splits > 1)
+            store_row32(p.partial + (static_cast<long long>(w.split) * p.n + row) * p.k + j, v, p.k - j, false);
+          else
+            store_row32(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + j, v, p.k - j, p.accumulate != 0);
+        }
+        __syncwarp();
+      }
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_u32(&tempty[acc]), 0));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  } else {
+    // ------------------------------------------------------ codes to bf16
+    // thread j restores the 16 codes 16 (j % 8).. of rows j / 8 and j / 8 + 32
+    const int j = threadIdx.x - 32 * (2 + WG_EPI_WARPS);
+    const int f = j & 7, tr = j >> 3;
+    // chunk f / 4, units 2 (f % 4) and the next; the upper chunk's lanes write
+    // their two units in the other order, so that the 8 lanes of a row touch
+    // 8 different 16-byte columns at a time
+    const int swap = f >> 2;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = first; u < p.units && ok; u += step) {
+      const WgUnit w = wg_unit(p, u);
+      const int blk = (w.k0 >> 7) + rank;
+      // exponents, read two stages ahead in the order of the unit's row
+      // blocks; 127 (any finite one) where the tensor map loads zeros
+      int tb = w.kb0 % p.row_blocks;
+      auto exponents = [&](int (&e)[2]) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const long long t = static_cast<long long>(tb) * WG_BK + tr + 32 * r;
+          e[r] = (t < p.rows && blk < p.nblk) ? p.exps[t * p.nblk + blk] : 127;
+        }
+        if (++tb == p.row_blocks) tb = 0;
+      };
+      int e0[2], e1[2];   // of this stage and the next
+      exponents(e0);
+      exponents(e1);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        int e2[2];
+        exponents(e2);
+        if (!__all_sync(0xffffffffu, sm100::mbar_wait(&full_q[stage], phase, abort_flag))) {
+          if (lane == 0) wg_timeout(p.status, abort_flag);
+          ok = false;
+          break;
+        }
+        uint8_t* sb = smem + stage * WG_STAGE + WG_A_BYTES;
+        const uint8_t* sq = sb + WG_B_BYTES;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int t = tr + 32 * r;
+          const uint4 q = *reinterpret_cast<const uint4*>(sq + t * 128 + f * 16);
+          uint4 v[2];
+          restore16(q, e0[r], v[0], v[1]);
+          uint8_t* dst = sb + (f >> 2) * WG_CHUNK + t * 128;
+          const int u0 = (f & 3) * 2;
+          *reinterpret_cast<uint4*>(dst + (((u0 + swap) ^ (t & 7)) << 4)) = swap ? v[1] : v[0];
+          *reinterpret_cast<uint4*>(dst + (((u0 + 1 - swap) ^ (t & 7)) << 4)) = swap ? v[0] : v[1];
+        }
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_u32(&ready[stage]), 0));
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          e0[r] = e1[r];
+          e1[r] = e2[r];
+        }
+        if (++stage == WG_STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  }
+
+  sm100::tc_fence_before();
+  __syncwarp();
+  sm100::cluster_sync();
+  sm100::tc_fence_after();
+  pdl_launch_dependents();
+  if (warp == 1) {
+    __syncwarp();
+    sm100::tmem_dealloc_pair(tmem, WG_TMEM);
+  }
+}
+
+// grad (+)= the units' sums, split 0 first; 4 elements per thread where rows
+// of 4 divide the matrix.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(256) weight_grad_join_kernel(const float* partial, G* grad, long long numel, int splits,
+                                                               int accumulate) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long e = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * VEC;
+  if (e >= numel) return;
+  float s[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) s[k] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < splits; ++i) {
+    const float* src = partial + i * numel + e;
+    if constexpr (VEC == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      s[0] += v.x;
+      s[1] += v.y;
+      s[2] += v.z;
+      s[3] += v.w;
+    } else {
+      s[0] += *src;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    if (accumulate) s[k] += to_f32(grad[e + k]);
+  }
+  if constexpr (VEC == 4 && sizeof(G) == 4) {
+    *reinterpret_cast<float4*>(grad + e) = make_float4(s[0], s[1], s[2], s[3]);
+  } else if constexpr (VEC == 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(s[0], s[1]), b = __floats2bfloat162_rn(s[2], s[3]);
+    *reinterpret_cast<uint2*>(grad + e) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    grad[e] = from_f32<G>(s[0]);
+  }
+}
+
+// dy -> bf16 planes [planes][rows][pitch] (pitch a multiple of 64, zeros past
+// n).  fp32: v = p0 + p1 + p2, each the 8 leading significant bits of what is
+// left (cut, not rounded: nothing overflows, and 3 x 8 bits hold all 24);
+// infinities and NaN go to plane 0 alone.
+template <typename D, int PLANES>
+__global__ void __launch_bounds__(256) weight_grad_stage_kernel(const D* dy, long long dy_ld, __nv_bfloat16* out,
+                                                                long long rows, int n, int pitch) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int per_row = pitch / 2;   // two columns per thread
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long t = i / per_row;
+  if (t >= rows) return;
+  const int c = static_cast<int>(i - t * per_row) * 2;
+  float v[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = c + k < n ? to_f32(dy[t * dy_ld + c + k]) : 0.f;
+#pragma unroll
+  for (int pl = 0; pl < PLANES; ++pl) {
+    uint32_t b[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      b[k] = isnan(v[k]) ? 0x7fffu : __float_as_uint(v[k]) >> 16;
+      v[k] = isfinite(v[k]) ? v[k] - __uint_as_float(b[k] << 16) : 0.f;
+    }
+    *reinterpret_cast<uint32_t*>(out + (static_cast<long long>(pl) * rows + t) * pitch + c) = b[0] | (b[1] << 16);
+  }
+}
+
+// ---------------------------------------------------------------- launchers
+template <typename G>
+static cudaError_t tc_launch(const WeightGradTc& p, int sms, cudaStream_t s) {
+  auto kern = weight_grad_tc_kernel<G>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(WG_THREADS);
+  cfg.dynamicSmemBytes = WG_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const int pairs = sms / 2;
+  cfg.gridDim = dim3(2 * (p.units < pairs ? p.units : pairs));
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+cudaError_t launch_weight_grad_tc(const WeightGradTc& p, int sms, cudaStream_t s) {
+  return p.grad_bf16 ? tc_launch<__nv_bfloat16>(p, sms, s) : tc_launch<float>(p, sms, s);
+}
+
+template <typename G>
+static cudaError_t join_launch(const WeightGradTc& p, cudaStream_t s) {
+  const long long numel = static_cast<long long>(p.n) * p.k;
+  G* g = static_cast<G*>(p.grad);
+  if (numel % 4 == 0)
+    return launch_pdl(weight_grad_join_kernel<G, 4>, dim3(static_cast<unsigned>((numel / 4 + 255) / 256)), dim3(256), 0, s,
+                      static_cast<const float*>(p.partial), g, numel, p.splits, p.accumulate);
+  return launch_pdl(weight_grad_join_kernel<G, 1>, dim3(static_cast<unsigned>((numel + 255) / 256)), dim3(256), 0, s,
+                    static_cast<const float*>(p.partial), g, numel, p.splits, p.accumulate);
+}
+cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s) {
+  return p.grad_bf16 ? join_launch<__nv_bfloat16>(p, s) : join_launch<float>(p, s);
+}
+
+cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,
+                                     int pitch, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((rows * (pitch / 2) + 255) / 256));
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+  if (bf16)
+    return launch_pdl(weight_grad_stage_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, s,
+                      static_cast<const __nv_bfloat16*>(dy), dy_ld, o, rows, n, pitch);
+  return launch_pdl(weight_grad_stage_kernel<float, 3>, grid, dim3(256), 0, s, static_cast<const float*>(dy), dy_ld, o,
+                    rows, n, pitch);
+}
+
+}  // namespace muon
