@@ -18,6 +18,9 @@ namespace {
 constexpr int64_t kMaxRows = 1ll << 30;      // tokens, activation rows
 constexpr int64_t kMaxVocab = 1ll << 30;
 constexpr int64_t kMaxDim = 65536;           // embedding and matrix widths
+// In stages of a weight gradient (64 rows of a tile, 0.55 us): the launch that
+// joins shared tiles, and each worker's sums written and read.
+constexpr double kWgJoinCost = 6.0, kWgPartCost = 0.2;
 constexpr int64_t kMaxTasks = 1ll << 33;     // warps of a launch (8 per block, 2^31 - 1 blocks)
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -110,38 +113,47 @@ muon_status check_checkpoint(const void* q, int64_t q_ld, const void* exps, int6
   return MUON_OK;
 }
 
-// Plan of a weight gradient: staging of dy and the split of its rows.
+// Plan of a weight gradient: staging of dy, and who sums what.
 struct WeightWs {
   int planes;      // bf16 planes dy is staged in (0: read as it is)
   int64_t pitch;   // of a staged row
-  int kblocks, splits;
+  int64_t tiles_n, tiles_k, tiles;
+  int kblocks, workers, whole_tiles;
+  bool shared;     // some tile is summed by several workers
   size_t staged, total;
 };
 WeightWs weight_ws(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype, bool dy_aligned) {
+  constexpr int kPairs = 74;   // CTA pairs of the GPU (148 SMs)
   WeightWs w = {};
   w.planes = dy_dtype == MUON_F32 ? 3 : dy_aligned ? 0 : 1;
   w.pitch = (n + 63) / 64 * 64;
   w.staged = up256(static_cast<size_t>(w.planes) * rows * w.pitch * 2);
-  const int64_t kb = (rows + 63) / 64 * std::max(w.planes, 1);
-  w.kblocks = static_cast<int>(kb);
-  // Split the rows so that the units fill the CTA pairs: the estimated time of
-  // a wave is its stages plus a fixed cost, and splits above one cost their
-  // sums' write and read and another launch (in units of one stage, 0.3 us).
-  const int64_t tiles = ((n + 255) / 256) * ((k + 255) / 256);
-  const int pairs = 74;
-  double best = 1e300;
-  w.splits = 1;
-  for (int64_t sp = 1; sp <= std::min<int64_t>(kb, 32); ++sp) {
-    if (sp > 1 && tiles * sp > 2 * pairs) break;
-    const double waves = static_cast<double>((tiles * sp + pairs - 1) / pairs);
-    const double join = sp == 1 ? 0.0 : 8.0 + static_cast<double>(sp) * n * k * 8.0 / (4e6 * 0.3);
-    const double cost = waves * (static_cast<double>((kb + sp - 1) / sp) + 10.0) + join;
-    if (cost < best) {
-      best = cost;
-      w.splits = static_cast<int>(sp);
+  w.kblocks = static_cast<int>((rows + 63) / 64 * std::max(w.planes, 1));
+  w.tiles_n = (n + kWgTileN - 1) / kWgTileN;
+  w.tiles_k = (k + kWgTileK - 1) / kWgTileK;
+  w.tiles = w.tiles_n * w.tiles_k;
+  if (w.tiles >= kPairs) {
+    // whole rounds of tiles, but for the last one and what is left after it
+    w.workers = kPairs;
+    const int64_t rounds = w.tiles / kPairs;
+    w.whole_tiles = static_cast<int>(w.tiles % kPairs == 0 ? w.tiles : (rounds - 1) * kPairs);
+  } else {
+    // Several workers per tile where that is faster: a worker's stages against
+    // the sums' write and read and a second launch.
+    w.whole_tiles = 0;
+    double best = 1e300;
+    for (int64_t per = 1; per <= std::max<int64_t>(w.kblocks, 1) && w.tiles * per <= kPairs; ++per) {
+      const double stages = static_cast<double>((w.kblocks + per - 1) / per);
+      const double join = per == 1 ? 0.0 : kWgJoinCost + static_cast<double>(w.tiles * per) * kWgPartCost;
+      if (stages + join < best) {
+        best = stages + join;
+        w.workers = static_cast<int>(w.tiles * per);
+      }
     }
   }
-  w.total = 256 + w.staged + (w.splits > 1 ? up256(static_cast<size_t>(w.splits) * n * k * 4) : 0);
+  w.shared = (w.tiles - w.whole_tiles) * w.kblocks % w.workers != 0 ||
+             (w.tiles - w.whole_tiles) * w.kblocks / w.workers % std::max(w.kblocks, 1) != 0;
+  w.total = 256 + w.staged + (w.shared ? static_cast<size_t>(2 * w.workers) * kWgTileN * kWgTileK * 4 : 0);
   return w;
 }
 }  // namespace
@@ -467,15 +479,16 @@ muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_
     p.nblk = (p.k + kCkptBlock - 1) / kCkptBlock;
     p.row_blocks = static_cast<int>((rows + 63) / 64);
     p.kblocks = w.kblocks;
-    p.tiles_n = (p.n + 255) / 256;
-    p.tiles_k = (p.k + 255) / 256;
-    p.splits = w.splits;
-    p.units = p.tiles_n * p.tiles_k * p.splits;
+    p.tiles_n = static_cast<int>(w.tiles_n);
+    p.tiles_k = static_cast<int>(w.tiles_k);
+    p.tiles = static_cast<int>(w.tiles);
+    p.workers = w.workers;
+    p.whole_tiles = w.whole_tiles;
     p.grad_bf16 = grad_dtype == MUON_BF16;
     p.accumulate = accumulate != 0;
-    st = launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad_tc(p, sms, s); }),
+    st = launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad_tc(p, s); }),
                   "weight gradient launch");
-    if (st != MUON_OK || p.splits == 1) return st;
+    if (st != MUON_OK || !w.shared) return st;
     return launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad_join(p, s); }),
                     "weight gradient join launch");
   });

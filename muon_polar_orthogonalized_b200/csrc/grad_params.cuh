@@ -74,19 +74,22 @@ struct CkptParams {
 };
 
 // The weight gradient on the tensor cores (k_weight_grad.cu).
+constexpr int kWgTileN = 512, kWgTileK = 256;   // dW rows (columns of dy) and features of a tile
 struct alignas(64) WeightGradTc {
   CUtensorMap tm_dy;   // bf16 dy: (n, rows, planes), or (64, rows, n / 64, planes) when chunked
   CUtensorMap tm_q;    // codes: (k, rows, 1)
   const uint8_t* exps;
   void* grad;          // [n, k]
-  float* partial;      // splits > 1: [splits][n][k]
+  float* partial;      // [2 * workers][kWgTileN][kWgTileK] sums of parts of tiles
   unsigned int* status;   // workspace word 0
   long long rows;
   int n, k, nblk;
   int chunked;
   int row_blocks;      // 64-row blocks of one plane
   int kblocks;         // planes * row_blocks
-  int tiles_n, tiles_k, splits, units;
+  int tiles_n, tiles_k, tiles;
+  int workers;         // CTA pairs
+  int whole_tiles;     // dealt out whole, tile i to worker i % workers; the rest by row blocks
   int grad_bf16, accumulate;
 };
 
@@ -102,7 +105,7 @@ cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s);
 cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s);
 cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,
                                      int pitch, cudaStream_t s);
-cudaError_t launch_weight_grad_tc(const WeightGradTc& p, int sms, cudaStream_t s);
+cudaError_t launch_weight_grad_tc(const WeightGradTc& p, cudaStream_t s);
 cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s);
 
 }  // namespace muon

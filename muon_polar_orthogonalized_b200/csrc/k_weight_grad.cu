@@ -11,24 +11,31 @@
 // shared memory and never exist in memory at 2 bytes: the kernel reads half
 // the bytes of x that a product of kept bf16 activations would.
 //
-// Structure: persistent CTA pairs (cta_group::2) on 256 x 256 tiles of dW.
-// Both operands are MN-major (their rows are the summed index).  Per 64 rows
-// and stage, each CTA brings by TMA 128 columns of dy (bf16, 128-byte swizzle:
-// the MMA operand as it stands) and 128 columns of codes (exactly one exponent
-// per row), and eight warps write the codes' bf16 values into the second
-// operand's swizzled layout.  The leader issues 256x256x16 MMAs into one of
-// two 256-column accumulators, so that a tile's epilogue overlaps the next
-// tile's MMAs.
-//   warp 0: TMA producer      warp 1: MMA issuer (+ TMEM owner)
-//   warps 2-5: epilogue       warps 6-13: codes to bf16
-// Four instructions and a packed multiply turn two codes into two bf16: the
-// code's exponent and mantissa bits, moved to the low end of bf16's exponent
-// and the high end of its mantissa, read as the value times 2^-120 (bf16
-// subnormals and the code's line up), so one exact multiply by a power of two
-// finishes it.
+// Structure: persistent CTA pairs (cta_group::2) on tiles of 512 columns of dy
+// by 256 features.  Both operands are MN-major (their rows are the summed
+// index).  Per 64 rows and stage, each CTA brings by TMA 2 x 128 columns of dy
+// (bf16, 128-byte swizzle: the MMA operand as it stands) and 128 features of
+// codes (exactly one exponent per row), and sixteen warps write the codes'
+// bf16 values into the second operand's swizzled layout.  The leader issues
+// 256x256x16 MMAs, two per 16 rows (one for each half of the dy columns), into
+// one 512-column accumulator: restored codes are used for 512 columns of dy,
+// which leaves the sixteen warps 1024 tensor-pipe cycles per stage.  (Tiles of
+// 256 columns with two accumulators leave 512, and measured 439 TFLOP/s with
+// eight restoring warps.)  The same sixteen warps write the finished tile.
+//   warp 0: TMA producer   warp 1: MMA issuer (+ TMEM owner)
+//   warps 2-17: codes to bf16, then the tile's epilogue
+// Three instructions turn two codes into two bf16 and a packed multiply
+// finishes them: the code's exponent and mantissa bits, moved to the low end
+// of bf16's exponent and the high end of its mantissa, read as the value times
+// 2^-120 (bf16 subnormals and the code's line up), so one exact multiply by a
+// power of two remains.  Bytes 1 and 3 of a word of four codes need no move to
+// their halves, so features 1 and 2 of every four change places in the
+// operand, and with them two registers in the epilogue.
 //
-// Few tiles, many rows: the rows are split over several units per tile, each
-// unit writes its fp32 sums to the workspace, and a second kernel adds them in
+// The (tile, row block) space is dealt out in whole tiles while there are
+// enough for every pair, and the rest in equal runs of row blocks that may
+// start and end inside a tile; a run that does not cover its tile writes fp32
+// sums to the workspace, and a second kernel adds the runs of such a tile in
 // order.  dy in fp32, or with rows that TMA cannot read, is first staged in
 // the workspace as bf16: one plane for bf16, three for fp32 (each value is
 // the sum of its three parts to the last bit), which the product walks one
@@ -45,50 +52,87 @@ namespace muon {
 
 namespace {
 constexpr int WG_BK = 64;                      // rows (summed index) per stage
-constexpr int WG_STAGES = 5;
-constexpr int WG_A_BYTES = 128 * WG_BK * 2;    // dy: two 64-column chunks
-constexpr int WG_B_BYTES = 128 * WG_BK * 2;    // restored x, likewise
-constexpr int WG_Q_BYTES = 128 * WG_BK;        // codes
+constexpr int WG_STAGES = 4;
 constexpr int WG_CHUNK = WG_BK * 128;          // one 64-column chunk of an operand
+constexpr int WG_SUB_BYTES = 2 * WG_CHUNK;     // dy: 128 columns of one half
+constexpr int WG_A_BYTES = 2 * WG_SUB_BYTES;
+constexpr int WG_B_BYTES = 2 * WG_CHUNK;       // restored x: 128 features
+constexpr int WG_Q_BYTES = 128 * WG_BK;        // codes
 constexpr int WG_STAGE = WG_A_BYTES + WG_B_BYTES + WG_Q_BYTES;
-constexpr int WG_EPI_WARPS = 4, WG_CVT_WARPS = 8;
-constexpr int WG_THREADS = 32 * (2 + WG_EPI_WARPS + WG_CVT_WARPS);
+constexpr int WG_WARPS = 16;                   // restoring and writing
+constexpr int WG_THREADS = 32 * (2 + WG_WARPS);
 constexpr int WG_BAR_OFF = WG_STAGES * WG_STAGE;
 constexpr int WG_SMEM = WG_BAR_OFF + 1024 + 1024;
 constexpr int WG_TMEM = 512;
 constexpr int WG_BAND = 8;                     // tile columns per raster band
 static_assert(WG_SMEM <= 232448, "shared memory per block");
 static_assert(WG_STAGE % 1024 == 0 && WG_A_BYTES % 1024 == 0, "swizzle atoms");
+static_assert(WG_WARPS * 32 == WG_BK * 8, "one 16-code task per thread and stage");
 constexpr uint32_t kTimeout = 1u;              // status word bit (muon_query_status)
 }  // namespace
 
+// One piece of a worker's work: row blocks [kb0, kb1) of a tile; slot >= 0
+// where they are not the whole tile.
 struct WgUnit {
-  int n0, k0, split, kb0, kb1;
+  int n0, k0, kb0, kb1, slot;
 };
 
-__device__ __forceinline__ WgUnit wg_unit(const WeightGradTc& p, int u) {
-  const int tiles = p.tiles_n * p.tiles_k;
-  const int split = u / tiles;
-  int r = u - split * tiles;
+__device__ __forceinline__ void wg_tile(const WeightGradTc& p, int tile, int& n0, int& k0) {
   const int band_tiles = p.tiles_n * WG_BAND;
-  const int band = r / band_tiles;
-  r -= band * band_tiles;
+  const int band = tile / band_tiles;
+  const int r = tile - band * band_tiles;
   const int width = min(WG_BAND, p.tiles_k - band * WG_BAND);
   const int tn = r / width;
-  const int tk = band * WG_BAND + (r - tn * width);
-  return {tn * 256, tk * 256, split, static_cast<int>(static_cast<long long>(p.kblocks) * split / p.splits),
-          static_cast<int>(static_cast<long long>(p.kblocks) * (split + 1) / p.splits)};
+  n0 = tn * kWgTileN;
+  k0 = (band * WG_BAND + (r - tn * width)) * kWgTileK;
 }
 
-// Two codes in bytes 1 and 3 of x, as two bf16 times 2^-120.
-__device__ __forceinline__ uint32_t code_bits(uint32_t x) { return ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u); }
+// First (tile, row block) of worker w's run over the dealt-out tiles, counted
+// from the first of them.
+__device__ __forceinline__ long long wg_run(const WeightGradTc& p, int w) {
+  return static_cast<long long>(p.tiles - p.whole_tiles) * p.kblocks * w / p.workers;
+}
+
+// A worker's pieces in order; every role walks the same list.
+struct WgWalk {
+  int w, next_tile;
+  long long pos, end;
+  bool first;
+  __device__ __forceinline__ explicit WgWalk(const WeightGradTc& p)
+      : w(blockIdx.x >> 1), next_tile(blockIdx.x >> 1), pos(wg_run(p, w)), end(wg_run(p, w + 1)), first(true) {}
+  __device__ __forceinline__ bool next(const WeightGradTc& p, WgUnit& u) {
+    if (next_tile < p.whole_tiles) {
+      wg_tile(p, next_tile, u.n0, u.k0);
+      u.kb0 = 0;
+      u.kb1 = p.kblocks;
+      u.slot = -1;
+      next_tile += p.workers;
+      return true;
+    }
+    if (pos >= end) return false;
+    const int t = static_cast<int>(pos / p.kblocks);
+    const long long base = static_cast<long long>(t) * p.kblocks;
+    wg_tile(p, p.whole_tiles + t, u.n0, u.k0);
+    u.kb0 = static_cast<int>(pos - base);
+    u.kb1 = static_cast<int>(min(end - base, static_cast<long long>(p.kblocks)));
+    u.slot = (u.kb0 == 0 && u.kb1 == p.kblocks) ? -1 : 2 * w + (first ? 0 : 1);
+    first = false;
+    pos = base + u.kb1;
+    return true;
+  }
+};
+
+// Codes in bytes 1 and 3 (bytes 0 and 2) of w as two bf16 times 2^-120.
+__device__ __forceinline__ uint32_t codes13(uint32_t w) { return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u); }
+__device__ __forceinline__ uint32_t codes02(uint32_t w) { return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u); }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t f) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// 16 codes of one exponent -> 16 bf16 in two 16-byte units.
+// 16 codes of one exponent -> 16 bf16 in two 16-byte units, features 1 and 2
+// of every four exchanged.
 __device__ __forceinline__ void restore16(const uint4& q, int e, uint4& lo, uint4& hi) {
   // 2^(120 + e - 127) fits bf16 up to e = 134; beyond, a second factor follows
   const int p = e == 255 ? 0 : min(e - 7, 127);
@@ -98,8 +142,8 @@ __device__ __forceinline__ void restore16(const uint4& q, int e, uint4& lo, uint
   uint32_t r[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    r[2 * i] = mul_bf16x2(code_bits(__byte_perm(w[i], 0, 0x1404)), f);
-    r[2 * i + 1] = mul_bf16x2(code_bits(__byte_perm(w[i], 0, 0x3424)), f);
+    r[2 * i] = mul_bf16x2(codes02(w[i]), f);
+    r[2 * i + 1] = mul_bf16x2(codes13(w[i]), f);
   }
   if (e > 134 && e != 255) {
     uint32_t g = static_cast<uint32_t>(e - 134 + 127) << 7;
@@ -173,26 +217,23 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   uint64_t* full_q = full_a + WG_STAGES;                               // this CTA's codes
   uint64_t* ready = full_q + WG_STAGES;                                // leader's: both CTAs' restored x
   uint64_t* empty = ready + WG_STAGES;
-  uint64_t* tfull = empty + WG_STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* tfull = empty + WG_STAGES;                                 // accumulator complete
+  uint64_t* tempty = tfull + 1;                                        // leader's: both CTAs' drained
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(sm100::cluster_ctarank());
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < WG_STAGES; ++s) {
       sm100::mbar_init(&full_a[s], 1);
       sm100::mbar_init(&full_q[s], 1);
-      sm100::mbar_init(&ready[s], 2 * WG_CVT_WARPS);
+      sm100::mbar_init(&ready[s], 2 * WG_WARPS);
       sm100::mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      sm100::mbar_init(&tfull[b], 1);
-      sm100::mbar_init(&tempty[b], 2 * WG_EPI_WARPS);
-    }
+    sm100::mbar_init(tfull, 1);
+    sm100::mbar_init(tempty, 2 * WG_WARPS);
     *abort_flag = 0;
     sm100::fence_mbar_init();
     sm100::prefetch_tmap(&p.tm_dy);
@@ -211,16 +252,18 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   // a wait that gives up does so seconds after this
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
+  WgWalk walk(p);
+  WgUnit u;
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
-      for (int u = first; u < p.units && ok; u += step) {
-        const WgUnit w = wg_unit(p, u);
-        const int nrow = w.n0 + rank * 128, kcol = w.k0 + rank * 128;
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+      while (ok && walk.next(p, u)) {
+        const int nact = u.n0 + 256 < p.n ? 2 : 1;   // halves of the tile with columns of dy
+        const int kcol = u.k0 + rank * 128;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
             wg_timeout(p.status, abort_flag);
             ok = false;
@@ -230,17 +273,21 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
           const int t0 = (kb - plane * p.row_blocks) * WG_BK;
           uint8_t* sa = smem + stage * WG_STAGE;
           uint8_t* sq = sa + WG_A_BYTES + WG_B_BYTES;
-          if (rank == 0) sm100::mbar_arrive_expect_tx(&full_a[stage], 2 * WG_A_BYTES);
           sm100::mbar_arrive_expect_tx(&full_q[stage], WG_Q_BYTES);
+          if (rank == 0) sm100::mbar_arrive_expect_tx(&full_a[stage], 2 * nact * WG_SUB_BYTES);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           sm100::tma_load_3d(sq, &p.tm_q, &full_q[stage], kcol, t0, 0);
           const uint32_t bar = sm100::mapa_shared(sm100::smem_u32(&full_a[stage]), 0);
-          if (p.chunked) {
-            sm100::tma_load_4d_pair(sa, &p.tm_dy, bar, 0, t0, nrow / 64, plane);
-          } else {
-            sm100::tma_load_3d_pair(sa, &p.tm_dy, bar, nrow, t0, plane);
-            sm100::tma_load_3d_pair(sa + WG_CHUNK, &p.tm_dy, bar, nrow + 64, t0, plane);
+          for (int h = 0; h < nact; ++h) {
+            const int col = u.n0 + h * 256 + rank * 128;
+            uint8_t* dst = sa + h * WG_SUB_BYTES;
+            if (p.chunked) {
+              sm100::tma_load_4d_pair(dst, &p.tm_dy, bar, 0, t0, col / 64, plane);
+            } else {
+              sm100::tma_load_3d_pair(dst, &p.tm_dy, bar, col, t0, plane);
+              sm100::tma_load_3d_pair(dst + WG_CHUNK, &p.tm_dy, bar, col + 64, t0, plane);
+            }
           }
           if (++stage == WG_STAGES) {
             stage = 0;
@@ -264,18 +311,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = sm100::make_idesc_bf16(256, 256, 1, 1);
-      int stage = 0, acc = 0;
+      int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int u = first; u < p.units && ok; u += step) {
-        const WgUnit w = wg_unit(p, u);
-        if (!sm100::mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
+      while (ok && walk.next(p, u)) {
+        const int nact = u.n0 + 256 < p.n ? 2 : 1;
+        if (!sm100::mbar_wait(tempty, acc_phase ^ 1u, abort_flag)) {
           wg_timeout(p.status, abort_flag);
           break;
         }
         sm100::tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!sm100::mbar_wait(&full_a[stage], phase, abort_flag) ||
               !sm100::mbar_wait(&ready[stage], phase, abort_flag)) {
             wg_timeout(p.status, abort_flag);
@@ -288,8 +334,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
           const uint64_t bd = sm100::make_sdesc(sa + WG_A_BYTES, WG_CHUNK, 1024);
 #pragma unroll
           for (int kk = 0; kk < WG_BK / 16; ++kk)
-            sm100::umma_bf16_pair(d, ad + static_cast<uint64_t>(kk * (2048 >> 4)),
-                                  bd + static_cast<uint64_t>(kk * (2048 >> 4)), idesc, (kb > w.kb0 || kk) ? 1u : 0u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (h < nact)
+                sm100::umma_bf16_pair(tmem + static_cast<uint32_t>(h * 256),
+                                      ad + static_cast<uint64_t>((h * WG_SUB_BYTES + kk * 2048) >> 4),
+                                      bd + static_cast<uint64_t>((kk * 2048) >> 4), idesc,
+                                      (kb > u.kb0 || kk) ? 1u : 0u);
           sm100::umma_commit_pair_both(&empty[stage]);
           if (++stage == WG_STAGES) {
             stage = 0;
@@ -297,116 +348,96 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
           }
         }
         if (!ok) break;
-        sm100::umma_commit_pair_both(&tfull[acc]);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
-      }
-    }
-  } else if (warp < 2 + WG_EPI_WARPS) {
-    // ----------------------------------------------------------- epilogue
-    const int quad = warp & 3;
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int u = first; u < p.units; u += step) {
-      const WgUnit w = wg_unit(p, u);
-      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&tfull[acc], acc_phase, abort_flag))) {
-        if (lane == 0) wg_timeout(p.status, abort_flag);
-        break;
-      }
-      sm100::tc_fence_after();
-      const int row = w.n0 + rank * 128 + quad * 32 + lane;
-      const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256);
-      const int nch = min(8, (p.k - w.k0 + 31) / 32);
-#pragma unroll 1
-      for (int c = 0; c < nch; ++c) {
-        uint32_t r[32];
-        sm100::tmem_ld32_async(t_row + static_cast<uint32_t>(c * 32), r);
-        sm100::tmem_wait_ld(r);
-        if (row < p.n) {
-          float v[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
-          const int j = w.k0 + c * 32;
-          if (p.splits > 1)
-            store_row32(p.partial + (static_cast<long long>(w.split) * p.n + row) * p.k + j, v, p.k - j, false);
-          else
-            store_row32(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + j, v, p.k - j, p.accumulate != 0);
-        }
-        __syncwarp();
-      }
-      sm100::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_u32(&tempty[acc]), 0));
-      if (++acc == 2) {
-        acc = 0;
+        sm100::umma_commit_pair_both(tfull);
         acc_phase ^= 1u;
       }
     }
   } else {
-    // ------------------------------------------------------ codes to bf16
-    // thread j restores the 16 codes 16 (j % 8).. of rows j / 8 and j / 8 + 32
-    const int j = threadIdx.x - 32 * (2 + WG_EPI_WARPS);
-    const int f = j & 7, tr = j >> 3;
-    // chunk f / 4, units 2 (f % 4) and the next; the upper chunk's lanes write
-    // their two units in the other order, so that the 8 lanes of a row touch
-    // 8 different 16-byte columns at a time
+    // ---------------------------------------- codes to bf16, then the tile
+    // thread j restores codes 16 (j % 8) .. + 15 of row j / 8 of every stage
+    const int j = threadIdx.x - 64;
+    const int f = j & 7, t = j >> 3;
+    // their place: chunk f / 4, units 2 (f % 4) and the next; the upper chunk's
+    // lanes write their two units in the other order, so that the 8 lanes of a
+    // row touch 8 different 16-byte columns at a time
     const int swap = f >> 2;
+    const uint32_t src = WG_A_BYTES + WG_B_BYTES + t * 128 + f * 16;
+    const uint32_t dst = WG_A_BYTES + (f >> 2) * WG_CHUNK + t * 128;
+    const uint32_t dst0 = dst + ((((f & 3) * 2 + swap) ^ (t & 7)) << 4);
+    const uint32_t dst1 = dst + ((((f & 3) * 2 + 1 - swap) ^ (t & 7)) << 4);
+    const uint32_t ready0 = sm100::mapa_shared(sm100::smem_u32(ready), 0);
+    const uint32_t tempty0 = sm100::mapa_shared(sm100::smem_u32(tempty), 0);
+    const int quad = warp & 3, slice = (warp - 2) >> 2;
     int stage = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int u = first; u < p.units && ok; u += step) {
-      const WgUnit w = wg_unit(p, u);
-      const int blk = (w.k0 >> 7) + rank;
+    while (ok && walk.next(p, u)) {
+      const int blk = (u.k0 >> 7) + rank;
       // exponents, read two stages ahead in the order of the unit's row
       // blocks; 127 (any finite one) where the tensor map loads zeros
-      int tb = w.kb0 % p.row_blocks;
-      auto exponents = [&](int (&e)[2]) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const long long t = static_cast<long long>(tb) * WG_BK + tr + 32 * r;
-          e[r] = (t < p.rows && blk < p.nblk) ? p.exps[t * p.nblk + blk] : 127;
-        }
+      int tb = u.kb0 % p.row_blocks;
+      auto exponent = [&]() -> int {
+        const long long row = static_cast<long long>(tb) * WG_BK + t;
         if (++tb == p.row_blocks) tb = 0;
+        return (row < p.rows && blk < p.nblk) ? p.exps[row * p.nblk + blk] : 127;
       };
-      int e0[2], e1[2];   // of this stage and the next
-      exponents(e0);
-      exponents(e1);
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        int e2[2];
-        exponents(e2);
+      int e0 = exponent(), e1 = exponent();   // of this stage and the next
+      for (int kb = u.kb0; kb < u.kb1; ++kb) {
+        const int e2 = exponent();
         if (!__all_sync(0xffffffffu, sm100::mbar_wait(&full_q[stage], phase, abort_flag))) {
           if (lane == 0) wg_timeout(p.status, abort_flag);
           ok = false;
           break;
         }
-        uint8_t* sb = smem + stage * WG_STAGE + WG_A_BYTES;
-        const uint8_t* sq = sb + WG_B_BYTES;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int t = tr + 32 * r;
-          const uint4 q = *reinterpret_cast<const uint4*>(sq + t * 128 + f * 16);
-          uint4 v[2];
-          restore16(q, e0[r], v[0], v[1]);
-          uint8_t* dst = sb + (f >> 2) * WG_CHUNK + t * 128;
-          const int u0 = (f & 3) * 2;
-          *reinterpret_cast<uint4*>(dst + (((u0 + swap) ^ (t & 7)) << 4)) = swap ? v[1] : v[0];
-          *reinterpret_cast<uint4*>(dst + (((u0 + 1 - swap) ^ (t & 7)) << 4)) = swap ? v[0] : v[1];
-        }
+        uint8_t* base = smem + stage * WG_STAGE;
+        const uint4 q = *reinterpret_cast<const uint4*>(base + src);
+        uint4 lo, hi;
+        restore16(q, e0, lo, hi);
+        *reinterpret_cast<uint4*>(base + dst0) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(base + dst1) = swap ? lo : hi;
         sm100::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_u32(&ready[stage]), 0));
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          e0[r] = e1[r];
-          e1[r] = e2[r];
-        }
+        if (lane == 0) sm100::mbar_arrive_cluster(ready0 + stage * 8);
+        e0 = e1;
+        e1 = e2;
         if (++stage == WG_STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
+      if (!ok) break;
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(tfull, acc_phase, abort_flag))) {
+        if (lane == 0) wg_timeout(p.status, abort_flag);
+        break;
+      }
+      sm100::tc_fence_after();
+      acc_phase ^= 1u;
+      const int nact = u.n0 + 256 < p.n ? 2 : 1;
+#pragma unroll 1
+      for (int c = slice; c < 8 * nact; c += 4) {   // 32-column chunks of the 512 accumulator columns
+        const int row = u.n0 + (c >> 3) * 256 + rank * 128 + quad * 32 + lane;
+        const int col = u.k0 + (c & 7) * 32;
+        if (col >= p.k) continue;
+        uint32_t r[32];
+        sm100::tmem_ld32_async(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c * 32), r);
+        sm100::tmem_wait_ld(r);
+        if (row < p.n) {
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k)   // features 1 and 2 of every four back in place
+            v[k] = __uint_as_float(r[(k & 3) == 1 ? k + 1 : (k & 3) == 2 ? k - 1 : k]);
+          if (u.slot >= 0)
+            store_row32(p.partial + (static_cast<long long>(u.slot) * kWgTileN + (row - u.n0)) * kWgTileK + (c & 7) * 32, v,
+                        32, false);
+          else
+            store_row32(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + col, v, p.k - col,
+                        p.accumulate != 0);
+        }
+        __syncwarp();
+      }
+      sm100::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive_cluster(tempty0);
     }
   }
 
@@ -421,42 +452,53 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   }
 }
 
-// grad (+)= the units' sums, split 0 first; 4 elements per thread where rows
-// of 4 divide the matrix.
-template <typename G, int VEC>
-__global__ void __launch_bounds__(256) weight_grad_join_kernel(const float* partial, G* grad, long long numel, int splits,
-                                                               int accumulate) {
+// grad (+)= the runs' sums of each tile that several workers share, in the
+// order of their rows.  Block (b, y): the tile that the start of worker b + 1's
+// run lies inside, if it is the first start inside it; rows 4 y .. 4 y + 3.
+template <typename G>
+__global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_constant__ WeightGradTc p) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long e = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * VEC;
-  if (e >= numel) return;
-  float s[VEC];
-#pragma unroll
-  for (int k = 0; k < VEC; ++k) s[k] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < splits; ++i) {
-    const float* src = partial + i * numel + e;
-    if constexpr (VEC == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      s[0] += v.x;
-      s[1] += v.y;
-      s[2] += v.z;
-      s[3] += v.w;
+  const int w1 = blockIdx.x + 1;
+  const long long at = wg_run(p, w1);
+  const int t = static_cast<int>(at / p.kblocks);
+  const long long t0 = static_cast<long long>(t) * p.kblocks, t1 = t0 + p.kblocks;
+  if (at == t0 || wg_run(p, w1 - 1) > t0) return;
+  int n0, k0;
+  wg_tile(p, p.whole_tiles + t, n0, k0);
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+  const int row = n0 + r, col = k0 + c;
+  if (row >= p.n || col >= p.k) return;
+  float s[4] = {};
+  for (int w = w1 - 1; w < p.workers; ++w) {
+    const long long b = wg_run(p, w);
+    if (b >= t1) break;
+    // a run's first tile is the one its start lies in
+    const int slot = 2 * w + (b >= t0 ? 0 : (b / p.kblocks == t ? 0 : 1));
+    const float4 v = *reinterpret_cast<const float4*>(
+        p.partial + (static_cast<long long>(slot) * kWgTileN + r) * kWgTileK + c);
+    s[0] += v.x;
+    s[1] += v.y;
+    s[2] += v.z;
+    s[3] += v.w;
+  }
+  G* out = static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + col;
+  if (col + 4 <= p.k && p.k % 4 == 0) {
+    if constexpr (sizeof(G) == 4) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.accumulate) o = *reinterpret_cast<const float4*>(out);
+      *reinterpret_cast<float4*>(out) = make_float4(o.x + s[0], o.y + s[1], o.z + s[2], o.w + s[3]);
     } else {
-      s[0] += *src;
-    }
-  }
+      if (p.accumulate)
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) {
-    if (accumulate) s[k] += to_f32(grad[e + k]);
-  }
-  if constexpr (VEC == 4 && sizeof(G) == 4) {
-    *reinterpret_cast<float4*>(grad + e) = make_float4(s[0], s[1], s[2], s[3]);
-  } else if constexpr (VEC == 4) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(s[0], s[1]), b = __floats2bfloat162_rn(s[2], s[3]);
-    *reinterpret_cast<uint2*>(grad + e) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        for (int k = 0; k < 4; ++k) s[k] += to_f32(out[k]);
+      const __nv_bfloat162 a = __floats2bfloat162_rn(s[0], s[1]), b = __floats2bfloat162_rn(s[2], s[3]);
+      *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
   } else {
-    grad[e] = from_f32<G>(s[0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (col + k < p.k) out[k] = from_f32<G>(s[k] + (p.accumulate ? to_f32(out[k]) : 0.f));
   }
 }
 
@@ -491,7 +533,7 @@ __global__ void __launch_bounds__(256) weight_grad_stage_kernel(const D* dy, lon
 
 // ---------------------------------------------------------------- launchers
 template <typename G>
-static cudaError_t tc_launch(const WeightGradTc& p, int sms, cudaStream_t s) {
+static cudaError_t tc_launch(const WeightGradTc& p, cudaStream_t s) {
   auto kern = weight_grad_tc_kernel<G>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM);
   if (e != cudaSuccess) return e;
@@ -508,26 +550,17 @@ static cudaError_t tc_launch(const WeightGradTc& p, int sms, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const int pairs = sms / 2;
-  cfg.gridDim = dim3(2 * (p.units < pairs ? p.units : pairs));
+  cfg.gridDim = dim3(2 * p.workers);
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
-cudaError_t launch_weight_grad_tc(const WeightGradTc& p, int sms, cudaStream_t s) {
-  return p.grad_bf16 ? tc_launch<__nv_bfloat16>(p, sms, s) : tc_launch<float>(p, sms, s);
+cudaError_t launch_weight_grad_tc(const WeightGradTc& p, cudaStream_t s) {
+  return p.grad_bf16 ? tc_launch<__nv_bfloat16>(p, s) : tc_launch<float>(p, s);
 }
 
-template <typename G>
-static cudaError_t join_launch(const WeightGradTc& p, cudaStream_t s) {
-  const long long numel = static_cast<long long>(p.n) * p.k;
-  G* g = static_cast<G*>(p.grad);
-  if (numel % 4 == 0)
-    return launch_pdl(weight_grad_join_kernel<G, 4>, dim3(static_cast<unsigned>((numel / 4 + 255) / 256)), dim3(256), 0, s,
-                      static_cast<const float*>(p.partial), g, numel, p.splits, p.accumulate);
-  return launch_pdl(weight_grad_join_kernel<G, 1>, dim3(static_cast<unsigned>((numel + 255) / 256)), dim3(256), 0, s,
-                    static_cast<const float*>(p.partial), g, numel, p.splits, p.accumulate);
-}
 cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s) {
-  return p.grad_bf16 ? join_launch<__nv_bfloat16>(p, s) : join_launch<float>(p, s);
+  const dim3 grid(p.workers - 1, kWgTileN / 4);
+  return p.grad_bf16 ? launch_pdl(weight_grad_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p)
+                     : launch_pdl(weight_grad_join_kernel<float>, grid, dim3(256), 0, s, p);
 }
 
 cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,

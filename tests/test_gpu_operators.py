@@ -397,7 +397,8 @@ def wg_checkpoint(rows, k, seed, dev, kind):
 
 
 @pytest.mark.parametrize("ddt", [BF16, F32])
-@pytest.mark.parametrize("rows,n,k", WG_SHAPES)
+@pytest.mark.parametrize("rows,n,k", WG_SHAPES + [(4001, 250, 500), (130, 4096, 2560), (200, 5001, 2500), (70, 9472, 1024),
+                                                  (321, 8200, 3000)])
 def test_weight_grad_of_whole_numbers_is_exact(dev, ddt, rows, n, k):
     ck, values = wg_checkpoint(rows, k, 50, dev, "whole")
     dy = whole((rows, n), -4, 4, ddt, 51, dev)
