@@ -215,8 +215,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + WG_BAR_OFF);   // leader's: both CTAs' dy
   uint64_t* full_q = full_a + WG_STAGES;                               // this CTA's codes
-  uint64_t* ready = full_q + WG_STAGES;                                // leader's: both CTAs' restored x
-  uint64_t* empty = ready + WG_STAGES;
+  uint64_t* ready = full_q + WG_STAGES;                                // this CTA's restored x
+  uint64_t* peer_ready = ready + WG_STAGES;                            // leader's: the other CTA's
+  uint64_t* empty = peer_ready + WG_STAGES;
   uint64_t* tfull = empty + WG_STAGES;                                 // accumulator complete
   uint64_t* tempty = tfull + 1;                                        // leader's: both CTAs' drained
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
@@ -229,7 +230,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     for (int s = 0; s < WG_STAGES; ++s) {
       sm100::mbar_init(&full_a[s], 1);
       sm100::mbar_init(&full_q[s], 1);
-      sm100::mbar_init(&ready[s], 2 * WG_WARPS);
+      sm100::mbar_init(&ready[s], WG_WARPS);
+      sm100::mbar_init(&peer_ready[s], 1);
       sm100::mbar_init(&empty[s], 1);
     }
     sm100::mbar_init(tfull, 1);
@@ -323,7 +325,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
         sm100::tc_fence_after();
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!sm100::mbar_wait(&full_a[stage], phase, abort_flag) ||
-              !sm100::mbar_wait(&ready[stage], phase, abort_flag)) {
+              !sm100::mbar_wait(&ready[stage], phase, abort_flag) ||
+              !sm100::mbar_wait(&peer_ready[stage], phase, abort_flag)) {
             wg_timeout(p.status, abort_flag);
             ok = false;
             break;
@@ -351,6 +354,28 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
         sm100::umma_commit_pair_both(tfull);
         acc_phase ^= 1u;
       }
+    } else if (lane == 0) {
+      // The other CTA's issuer relays its restored stages to the leader.  (An
+      // arrival on another CTA's barrier releases at cluster scope, which
+      // waits for the thread's loads in flight too: sent by the restoring
+      // warps themselves it made every stage wait for their exponents.)
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && walk.next(p, u)) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!sm100::mbar_wait(&ready[stage], phase, abort_flag)) {
+            wg_timeout(p.status, abort_flag);
+            ok = false;
+            break;
+          }
+          sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_u32(&peer_ready[stage]), 0));
+          if (++stage == WG_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
     }
   } else {
     // ---------------------------------------- codes to bf16, then the tile
@@ -365,7 +390,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     const uint32_t dst = WG_A_BYTES + (f >> 2) * WG_CHUNK + t * 128;
     const uint32_t dst0 = dst + ((((f & 3) * 2 + swap) ^ (t & 7)) << 4);
     const uint32_t dst1 = dst + ((((f & 3) * 2 + 1 - swap) ^ (t & 7)) << 4);
-    const uint32_t ready0 = sm100::mapa_shared(sm100::smem_u32(ready), 0);
     const uint32_t tempty0 = sm100::mapa_shared(sm100::smem_u32(tempty), 0);
     const int quad = warp & 3, slice = (warp - 2) >> 2;
     int stage = 0;
@@ -373,37 +397,47 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     bool ok = true;
     while (ok && walk.next(p, u)) {
       const int blk = (u.k0 >> 7) + rank;
-      // exponents, read two stages ahead in the order of the unit's row
-      // blocks; 127 (any finite one) where the tensor map loads zeros
+      // Exponents in the order of the unit's row blocks; 127 (any finite one)
+      // where the tensor map loads zeros.  Read four stages at a time, four
+      // ahead: a register that a load is still filling must not be touched, a
+      // copy included, or every stage waits out the load (1.3 us a stage
+      // with a two-deep shift register, at any amount of work per stage).
       int tb = u.kb0 % p.row_blocks;
       auto exponent = [&]() -> int {
         const long long row = static_cast<long long>(tb) * WG_BK + t;
         if (++tb == p.row_blocks) tb = 0;
         return (row < p.rows && blk < p.nblk) ? p.exps[row * p.nblk + blk] : 127;
       };
-      int e0 = exponent(), e1 = exponent();   // of this stage and the next
-      for (int kb = u.kb0; kb < u.kb1; ++kb) {
-        const int e2 = exponent();
-        if (!__all_sync(0xffffffffu, sm100::mbar_wait(&full_q[stage], phase, abort_flag))) {
-          if (lane == 0) wg_timeout(p.status, abort_flag);
-          ok = false;
-          break;
+      int e[4], e_next[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = exponent();
+      for (int kb4 = u.kb0; ok && kb4 < u.kb1; kb4 += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e_next[i] = exponent();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (kb4 + i >= u.kb1) break;
+          if (!__all_sync(0xffffffffu, sm100::mbar_wait(&full_q[stage], phase, abort_flag))) {
+            if (lane == 0) wg_timeout(p.status, abort_flag);
+            ok = false;
+            break;
+          }
+          uint8_t* base = smem + stage * WG_STAGE;
+          const uint4 q = *reinterpret_cast<const uint4*>(base + src);
+          uint4 lo, hi;
+          restore16(q, e[i], lo, hi);
+          *reinterpret_cast<uint4*>(base + dst0) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(base + dst1) = swap ? lo : hi;
+          sm100::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&ready[stage]);
+          if (++stage == WG_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        uint8_t* base = smem + stage * WG_STAGE;
-        const uint4 q = *reinterpret_cast<const uint4*>(base + src);
-        uint4 lo, hi;
-        restore16(q, e0, lo, hi);
-        *reinterpret_cast<uint4*>(base + dst0) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(base + dst1) = swap ? lo : hi;
-        sm100::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive_cluster(ready0 + stage * 8);
-        e0 = e1;
-        e1 = e2;
-        if (++stage == WG_STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = e_next[i];
       }
       if (!ok) break;
       if (!__all_sync(0xffffffffu, sm100::mbar_wait(tfull, acc_phase, abort_flag))) {
