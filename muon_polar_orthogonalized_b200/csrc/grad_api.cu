@@ -484,6 +484,9 @@ muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_
     p.tiles = static_cast<int>(w.tiles);
     p.workers = w.workers;
     p.whole_tiles = w.whole_tiles;
+    const int64_t blocks = (w.tiles - w.whole_tiles) * w.kblocks;
+    p.run_len = blocks / w.workers;
+    p.run_longer = static_cast<int>(blocks % w.workers);
     p.grad_bf16 = grad_dtype == MUON_BF16;
     p.accumulate = accumulate != 0;
     st = launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] { return launch_weight_grad_tc(p, s); }),

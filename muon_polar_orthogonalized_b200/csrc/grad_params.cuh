@@ -89,7 +89,9 @@ struct alignas(64) WeightGradTc {
   int kblocks;         // planes * row_blocks
   int tiles_n, tiles_k, tiles;
   int workers;         // CTA pairs
-  int whole_tiles;     // dealt out whole, tile i to worker i % workers; the rest by row blocks
+  int whole_tiles;     // dealt out whole, tile i to worker i % workers; the rest by row blocks:
+  long long run_len;   // row blocks of a run, and the workers whose run is one longer
+  int run_longer;
   int grad_bf16, accumulate;
 };
 

@@ -88,9 +88,15 @@ __device__ __forceinline__ void wg_tile(const WeightGradTc& p, int tile, int& n0
 }
 
 // First (tile, row block) of worker w's run over the dealt-out tiles, counted
-// from the first of them.
+// from the first of them: runs differ by one block at most, the longer first.
 __device__ __forceinline__ long long wg_run(const WeightGradTc& p, int w) {
-  return static_cast<long long>(p.tiles - p.whole_tiles) * p.kblocks * w / p.workers;
+  return p.run_len * w + min(w, p.run_longer);
+}
+// The dealt-out tile a position lies in (a 64-bit division takes as long as
+// half a stage's product).
+__device__ __forceinline__ int wg_run_tile(const WeightGradTc& p, long long pos) {
+  if (pos <= 0xffffffffll) return static_cast<int>(static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.kblocks));
+  return static_cast<int>(pos / p.kblocks);
 }
 
 // A worker's pieces in order; every role walks the same list.
@@ -110,7 +116,7 @@ struct WgWalk {
       return true;
     }
     if (pos >= end) return false;
-    const int t = static_cast<int>(pos / p.kblocks);
+    const int t = wg_run_tile(p, pos);
     const long long base = static_cast<long long>(t) * p.kblocks;
     wg_tile(p, p.whole_tiles + t, u.n0, u.k0);
     u.kb0 = static_cast<int>(pos - base);
@@ -155,51 +161,55 @@ __device__ __forceinline__ void restore16(const uint4& q, int e, uint4& lo, uint
   hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// One row's 32 columns of the output (fp32 or bf16), with 32-byte, 16-byte or
-// single accesses as its address and the columns left allow.
-template <typename G>
-__device__ __forceinline__ void store_row32(G* dst, const float (&v)[32], int cols, bool accumulate) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(dst);
-  if (cols >= 32 && (a & 15) == 0) {
-    float o[32];
-    if (accumulate) {
+// A warp's 32 x 32 block of sums, lane = row, to memory.  Stored from where it
+// is, every instruction would touch 32 rows (a drain of 8.8 us for a pair's
+// tile); so the 8-column pieces are first transposed among each four lanes
+// (two butterfly steps), after which lane l holds piece l % 4 of rows l & ~3
+// .. + 3 and an instruction fills whole 128-byte lines of 8 rows (fp32).
+__device__ __forceinline__ void transpose_pieces(float (&v)[4][8], int lane) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) load8(dst + 8 * k, *reinterpret_cast<float(*)[8]>(&o[8 * k]));
+  for (int b = 1; b <= 2; b <<= 1) {
+    const bool up = lane & b;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] += v[k];
-    } else {
+    for (int i = 0; i < 4; ++i) {
+      if (i & b) continue;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = v[k];
-    }
-    uint4 u[sizeof(G) * 2];
-    if constexpr (sizeof(G) == 2) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t w[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(o[8 * k + 2 * h], o[8 * k + 2 * h + 1]);
-          w[h] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < 8; ++k) {
+        const float send = up ? v[i][k] : v[i | b][k];
+        const float recv = __shfl_xor_sync(0xffffffffu, send, b);
+        if (up) v[i][k] = recv;
+        else v[i | b][k] = recv;
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        u[k] = make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
-                          __float_as_uint(o[4 * k + 3]));
     }
-    constexpr int N = sizeof(G) * 2;   // 16-byte units
-    if ((a & 31) == 0) {
+  }
+}
+
+// 8 sums as one whole 32-byte sector (dst 32-byte aligned).
+__device__ __forceinline__ void store_sector(float* dst, const float (&v)[8]) {
+  sm100::st_global_v8(dst, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
+                      make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+}
+
+// 8 columns of one row; vec: 16-byte accesses allowed and cols >= 8.
+template <typename G>
+__device__ __forceinline__ void store_piece(G* dst, float (&v)[8], int cols, bool accumulate, bool vec) {
+  if (vec) {
+    if (accumulate) {
+      float o[8];
+      load8(dst, o);
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) sm100::st_global_v8(reinterpret_cast<uint4*>(dst) + 2 * k, u[2 * k], u[2 * k + 1]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; ++k) reinterpret_cast<uint4*>(dst)[k] = u[k];
+      for (int k = 0; k < 8; ++k) v[k] += o[k];
     }
+    if constexpr (sizeof(G) == 4) {
+      if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+        store_sector(dst, v);
+        return;
+      }
+    }
+    store8(dst, v);
   } else {
 #pragma unroll
-    for (int k = 0; k < 32; ++k)
+    for (int k = 0; k < 8; ++k)
       if (k < cols) dst[k] = from_f32<G>(v[k] + (accumulate ? to_f32(dst[k]) : 0.f));
   }
 }
@@ -392,6 +402,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     const uint32_t dst1 = dst + ((((f & 3) * 2 + 1 - swap) ^ (t & 7)) << 4);
     const uint32_t tempty0 = sm100::mapa_shared(sm100::smem_u32(tempty), 0);
     const int quad = warp & 3, slice = (warp - 2) >> 2;
+    const bool vec = (static_cast<long long>(p.k) * sizeof(G)) % 16 == 0;   // grad is 16-byte aligned
     int stage = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
@@ -449,25 +460,28 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
       const int nact = u.n0 + 256 < p.n ? 2 : 1;
 #pragma unroll 1
       for (int c = slice; c < 8 * nact; c += 4) {   // 32-column chunks of the 512 accumulator columns
-        const int row = u.n0 + (c >> 3) * 256 + rank * 128 + quad * 32 + lane;
         const int col = u.k0 + (c & 7) * 32;
         if (col >= p.k) continue;
         uint32_t r[32];
         sm100::tmem_ld32_async(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c * 32), r);
         sm100::tmem_wait_ld(r);
-        if (row < p.n) {
-          float v[32];
+        float v[4][8];
 #pragma unroll
-          for (int k = 0; k < 32; ++k)   // features 1 and 2 of every four back in place
-            v[k] = __uint_as_float(r[(k & 3) == 1 ? k + 1 : (k & 3) == 2 ? k - 1 : k]);
+        for (int k = 0; k < 32; ++k)   // features 1 and 2 of every four back in place
+          v[k >> 3][k & 7] = __uint_as_float(r[(k & 3) == 1 ? k + 1 : (k & 3) == 2 ? k - 1 : k]);
+        transpose_pieces(v, lane);
+        const int row0 = u.n0 + (c >> 3) * 256 + rank * 128 + quad * 32 + (lane & ~3);
+        const int c0 = col + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = row0 + i;
+          if (row >= p.n) continue;
           if (u.slot >= 0)
-            store_row32(p.partial + (static_cast<long long>(u.slot) * kWgTileN + (row - u.n0)) * kWgTileK + (c & 7) * 32, v,
-                        32, false);
+            store_sector(p.partial + (static_cast<long long>(u.slot) * kWgTileN + (row - u.n0)) * kWgTileK + (c0 - u.k0), v[i]);
           else
-            store_row32(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + col, v, p.k - col,
-                        p.accumulate != 0);
+            store_piece(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + c0, v[i], p.k - c0,
+                        p.accumulate != 0, vec && c0 + 8 <= p.k);
         }
-        __syncwarp();
       }
       sm100::tc_fence_before();
       __syncwarp();
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
   pdl_wait();
   const int w1 = blockIdx.x + 1;
   const long long at = wg_run(p, w1);
-  const int t = static_cast<int>(at / p.kblocks);
+  const int t = wg_run_tile(p, at);
   const long long t0 = static_cast<long long>(t) * p.kblocks, t1 = t0 + p.kblocks;
   if (at == t0 || wg_run(p, w1 - 1) > t0) return;
   int n0, k0;
@@ -504,11 +518,11 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
   const int row = n0 + r, col = k0 + c;
   if (row >= p.n || col >= p.k) return;
   float s[4] = {};
-  for (int w = w1 - 1; w < p.workers; ++w) {
-    const long long b = wg_run(p, w);
-    if (b >= t1) break;
-    // a run's first tile is the one its start lies in
-    const int slot = 2 * w + (b >= t0 ? 0 : (b / p.kblocks == t ? 0 : 1));
+  int w_end = w1 + 1;
+  while (w_end < p.workers && wg_run(p, w_end) < t1) ++w_end;
+#pragma unroll 4
+  for (int w = w1 - 1; w < w_end; ++w) {
+    const int slot = 2 * w + (wg_run(p, w) >= t0 ? 0 : 1);   // 0: the tile its run starts in
     const float4 v = *reinterpret_cast<const float4*>(
         p.partial + (static_cast<long long>(slot) * kWgTileN + r) * kWgTileK + c);
     s[0] += v.x;
