@@ -18,9 +18,13 @@ namespace {
 constexpr int64_t kMaxRows = 1ll << 30;      // tokens, activation rows
 constexpr int64_t kMaxVocab = 1ll << 30;
 constexpr int64_t kMaxDim = 65536;           // embedding and matrix widths
-// In stages of a weight gradient (64 rows of a tile, 0.55 us): the launch that
-// joins shared tiles, and each worker's sums written and read.
-constexpr double kWgJoinCost = 6.0, kWgPartCost = 0.2;
+// Measured costs of a weight gradient's parts, in microseconds: a stage (64
+// rows of a tile), a tile's start and drain, the launch that joins shared
+// tiles, and each worker's sums written and read.
+struct WgCost {
+  double stage, tile, join, part;
+};
+constexpr WgCost kWgCost[2] = {{0.40, 6.5, 3.0, 0.02}, {0.66, 11.5, 4.0, 0.10}};   // narrow, wide
 constexpr int64_t kMaxTasks = 1ll << 33;     // warps of a launch (8 per block, 2^31 - 1 blocks)
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -113,47 +117,60 @@ muon_status check_checkpoint(const void* q, int64_t q_ld, const void* exps, int6
   return MUON_OK;
 }
 
-// Plan of a weight gradient: staging of dy, and who sums what.
+// Plan of a weight gradient: staging of dy, the tile, and who sums what.
 struct WeightWs {
   int planes;      // bf16 planes dy is staged in (0: read as it is)
   int64_t pitch;   // of a staged row
+  int wide;
   int64_t tiles_n, tiles_k, tiles;
   int kblocks, workers, whole_tiles;
   bool shared;     // some tile is summed by several workers
   size_t staged, total;
+  double cost;     // estimated microseconds
 };
-WeightWs weight_ws(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype, bool dy_aligned) {
+// The plan for one tile geometry.
+WeightWs weight_plan(WeightWs w, int wide, int64_t n, int64_t k) {
   constexpr int kPairs = 74;   // CTA pairs of the GPU (148 SMs)
-  WeightWs w = {};
-  w.planes = dy_dtype == MUON_F32 ? 3 : dy_aligned ? 0 : 1;
-  w.pitch = (n + 63) / 64 * 64;
-  w.staged = up256(static_cast<size_t>(w.planes) * rows * w.pitch * 2);
-  w.kblocks = static_cast<int>((rows + 63) / 64 * std::max(w.planes, 1));
-  w.tiles_n = (n + kWgTileN - 1) / kWgTileN;
-  w.tiles_k = (k + kWgTileK - 1) / kWgTileK;
+  const WgCost& c = kWgCost[wide];
+  w.wide = wide;
+  w.tiles_n = (n + kWgTile[wide].n - 1) / kWgTile[wide].n;
+  w.tiles_k = (k + kWgTile[wide].k - 1) / kWgTile[wide].k;
   w.tiles = w.tiles_n * w.tiles_k;
+  w.cost = 1e300;
   if (w.tiles >= kPairs) {
     // whole rounds of tiles, but for the last one and what is left after it
     w.workers = kPairs;
     const int64_t rounds = w.tiles / kPairs;
     w.whole_tiles = static_cast<int>(w.tiles % kPairs == 0 ? w.tiles : (rounds - 1) * kPairs);
+    const bool even = w.tiles % kPairs == 0;
+    w.cost = static_cast<double>(w.tiles) / kPairs * w.kblocks * c.stage + (even ? rounds : rounds + 1) * c.tile +
+             (even ? 0.0 : c.join + 2 * kPairs * c.part);
   } else {
-    // Several workers per tile where that is faster: a worker's stages against
-    // the sums' write and read and a second launch.
+    // several workers per tile where that is faster
     w.whole_tiles = 0;
-    double best = 1e300;
     for (int64_t per = 1; per <= std::max<int64_t>(w.kblocks, 1) && w.tiles * per <= kPairs; ++per) {
-      const double stages = static_cast<double>((w.kblocks + per - 1) / per);
-      const double join = per == 1 ? 0.0 : kWgJoinCost + static_cast<double>(w.tiles * per) * kWgPartCost;
-      if (stages + join < best) {
-        best = stages + join;
+      const double cost = static_cast<double>((w.kblocks + per - 1) / per) * c.stage + c.tile +
+                          (per == 1 ? 0.0 : c.join + static_cast<double>(w.tiles * per) * c.part);
+      if (cost < w.cost) {
+        w.cost = cost;
         w.workers = static_cast<int>(w.tiles * per);
       }
     }
   }
   w.shared = (w.tiles - w.whole_tiles) * w.kblocks % w.workers != 0 ||
              (w.tiles - w.whole_tiles) * w.kblocks / w.workers % std::max(w.kblocks, 1) != 0;
-  w.total = 256 + w.staged + (w.shared ? static_cast<size_t>(2 * w.workers) * kWgTileN * kWgTileK * 4 : 0);
+  return w;
+}
+WeightWs weight_ws(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype, bool dy_aligned) {
+  WeightWs w = {};
+  w.planes = dy_dtype == MUON_F32 ? 3 : dy_aligned ? 0 : 1;
+  w.pitch = (n + 63) / 64 * 64;
+  w.staged = up256(static_cast<size_t>(w.planes) * rows * w.pitch * 2);
+  w.kblocks = static_cast<int>((rows + 63) / 64 * std::max(w.planes, 1));
+  const WeightWs narrow = weight_plan(w, 0, n, k), wide = weight_plan(w, 1, n, k);
+  w = wide.cost <= narrow.cost ? wide : narrow;
+  w.total = 256 + w.staged +
+            (w.shared ? static_cast<size_t>(2 * w.workers) * kWgTile[w.wide].n * kWgTile[w.wide].k * 4 : 0);
   return w;
 }
 }  // namespace
@@ -464,7 +481,7 @@ muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_
     {
       const cuuint64_t dims[3] = {static_cast<cuuint64_t>(k), R, 1};
       const cuuint64_t strides[2] = {static_cast<cuuint64_t>(code_pitch), static_cast<cuuint64_t>(code_pitch)};
-      const cuuint32_t box[3] = {128, 64, 1};
+      const cuuint32_t box[3] = {static_cast<cuuint32_t>(kWgTile[w.wide].k / 2), 64, 1};
       st = api_tensor_map(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), dims, strides, box,
                           CU_TENSOR_MAP_SWIZZLE_NONE);
       if (st != MUON_OK) return st;
@@ -484,6 +501,7 @@ muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_
     p.tiles = static_cast<int>(w.tiles);
     p.workers = w.workers;
     p.whole_tiles = w.whole_tiles;
+    p.wide = w.wide;
     const int64_t blocks = (w.tiles - w.whole_tiles) * w.kblocks;
     p.run_len = blocks / w.workers;
     p.run_longer = static_cast<int>(blocks % w.workers);

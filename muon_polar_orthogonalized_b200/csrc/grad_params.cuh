@@ -74,17 +74,21 @@ struct CkptParams {
 };
 
 // The weight gradient on the tensor cores (k_weight_grad.cu).
-constexpr int kWgTileN = 512, kWgTileK = 256;   // dW rows (columns of dy) and features of a tile
+struct WgTile {
+  int n, k;            // dW rows (columns of dy) and features of a tile
+};
+constexpr WgTile kWgTile[2] = {{256, 128}, {512, 256}};   // narrow, wide
 struct alignas(64) WeightGradTc {
   CUtensorMap tm_dy;   // bf16 dy: (n, rows, planes), or (64, rows, n / 64, planes) when chunked
   CUtensorMap tm_q;    // codes: (k, rows, 1)
   const uint8_t* exps;
   void* grad;          // [n, k]
-  float* partial;      // [2 * workers][kWgTileN][kWgTileK] sums of parts of tiles
+  float* partial;      // [2 * workers][tile.n][tile.k] sums of parts of tiles
   unsigned int* status;   // workspace word 0
   long long rows;
   int n, k, nblk;
   int chunked;
+  int wide;            // tile geometry
   int row_blocks;      // 64-row blocks of one plane
   int kblocks;         // planes * row_blocks
   int tiles_n, tiles_k, tiles;

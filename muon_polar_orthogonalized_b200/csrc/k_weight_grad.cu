@@ -19,9 +19,14 @@
 // bf16 values into the second operand's swizzled layout.  The leader issues
 // 256x256x16 MMAs, two per 16 rows (one for each half of the dy columns), into
 // one 512-column accumulator: restored codes are used for 512 columns of dy,
-// which leaves the sixteen warps 1024 tensor-pipe cycles per stage.  (Tiles of
-// 256 columns with two accumulators leave 512, and measured 439 TFLOP/s with
-// eight restoring warps.)  The same sixteen warps write the finished tile.
+// which leaves the sixteen warps 1024 tensor-pipe cycles per stage.  The same
+// sixteen warps write the finished tile.  Measured: 1.46 PFLOP/s at 16384 x
+// 14336 x 4096 (1.32 ms, 1.08 of the measured sustained bf16 product, 0.90 of
+// its burst), 1.25 at 16384 x 1024 x 4096.  Where there are few tiles, or few
+// rows, a tile's start and drain (11 us) outweigh its product, and tiles of
+// 256 by 128 are used, on which two groups of eight warps take the stages in
+// turn: 12.0 us against 20.2 at 777 x 1664 x 768, but 0.65 PFLOP/s at the
+// large shapes.  The choice is by the estimated time (grad_api.cu).
 //   warp 0: TMA producer   warp 1: MMA issuer (+ TMEM owner)
 //   warps 2-17: codes to bf16, then the tile's epilogue
 // Three instructions turn two codes into two bf16 and a packed multiply
@@ -52,22 +57,35 @@ namespace muon {
 
 namespace {
 constexpr int WG_BK = 64;                      // rows (summed index) per stage
-constexpr int WG_STAGES = 4;
 constexpr int WG_CHUNK = WG_BK * 128;          // one 64-column chunk of an operand
-constexpr int WG_SUB_BYTES = 2 * WG_CHUNK;     // dy: 128 columns of one half
-constexpr int WG_A_BYTES = 2 * WG_SUB_BYTES;
-constexpr int WG_B_BYTES = 2 * WG_CHUNK;       // restored x: 128 features
-constexpr int WG_Q_BYTES = 128 * WG_BK;        // codes
-constexpr int WG_STAGE = WG_A_BYTES + WG_B_BYTES + WG_Q_BYTES;
+constexpr int WG_SUB_BYTES = 2 * WG_CHUNK;     // dy: 128 columns of one 256-column half
 constexpr int WG_WARPS = 16;                   // restoring and writing
 constexpr int WG_THREADS = 32 * (2 + WG_WARPS);
-constexpr int WG_BAR_OFF = WG_STAGES * WG_STAGE;
-constexpr int WG_SMEM = WG_BAR_OFF + 1024 + 1024;
-constexpr int WG_TMEM = 512;
 constexpr int WG_BAND = 8;                     // tile columns per raster band
-static_assert(WG_SMEM <= 232448, "shared memory per block");
-static_assert(WG_STAGE % 1024 == 0 && WG_A_BYTES % 1024 == 0, "swizzle atoms");
-static_assert(WG_WARPS * 32 == WG_BK * 8, "one 16-code task per thread and stage");
+
+// Tile geometry (kWgTile[wide]): 512 columns of dy by 256 features, or 256 by 128.
+template <bool WIDE>
+struct WgCfg {
+  static constexpr int TN = kWgTile[WIDE].n, TK = kWgTile[WIDE].k;
+  static constexpr int SUBS = TN / 256;                    // 256-column halves: MMAs per 16 rows
+  static constexpr int A_BYTES = SUBS * WG_SUB_BYTES;
+  static constexpr int CODES = TK / 2;                     // features per CTA
+  static constexpr int B_BYTES = CODES / 64 * WG_CHUNK;    // restored x
+  static constexpr int Q_BYTES = CODES * WG_BK;            // codes
+  static constexpr int STAGE = A_BYTES + B_BYTES + Q_BYTES;
+  static constexpr int STAGES = WIDE ? 4 : 7;
+  // a stage has WG_BK rows of CODES / 16 tasks of 16 codes, one per thread: the
+  // sixteen warps form GROUPS that take the stages in turn
+  static constexpr int ROW_TASKS = CODES / 16;
+  static constexpr int GROUP_WARPS = WG_BK * ROW_TASKS / 32;
+  static constexpr int GROUPS = WG_WARPS / GROUP_WARPS;
+  static constexpr int TMEM = SUBS * TK;                   // accumulator columns
+  static constexpr int BAR_OFF = STAGES * STAGE;
+  static constexpr int SMEM = BAR_OFF + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory per block");
+  static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(GROUPS * GROUP_WARPS == WG_WARPS && kCkptBlock % CODES == 0, "one exponent per row");
+};
 constexpr uint32_t kTimeout = 1u;              // status word bit (muon_query_status)
 }  // namespace
 
@@ -77,14 +95,15 @@ struct WgUnit {
   int n0, k0, kb0, kb1, slot;
 };
 
+template <bool WIDE>
 __device__ __forceinline__ void wg_tile(const WeightGradTc& p, int tile, int& n0, int& k0) {
   const int band_tiles = p.tiles_n * WG_BAND;
   const int band = tile / band_tiles;
   const int r = tile - band * band_tiles;
   const int width = min(WG_BAND, p.tiles_k - band * WG_BAND);
   const int tn = r / width;
-  n0 = tn * kWgTileN;
-  k0 = (band * WG_BAND + (r - tn * width)) * kWgTileK;
+  n0 = tn * kWgTile[WIDE].n;
+  k0 = (band * WG_BAND + (r - tn * width)) * kWgTile[WIDE].k;
 }
 
 // First (tile, row block) of worker w's run over the dealt-out tiles, counted
@@ -100,6 +119,7 @@ __device__ __forceinline__ int wg_run_tile(const WeightGradTc& p, long long pos)
 }
 
 // A worker's pieces in order; every role walks the same list.
+template <bool WIDE>
 struct WgWalk {
   int w, next_tile;
   long long pos, end;
@@ -108,7 +128,7 @@ struct WgWalk {
       : w(blockIdx.x >> 1), next_tile(blockIdx.x >> 1), pos(wg_run(p, w)), end(wg_run(p, w + 1)), first(true) {}
   __device__ __forceinline__ bool next(const WeightGradTc& p, WgUnit& u) {
     if (next_tile < p.whole_tiles) {
-      wg_tile(p, next_tile, u.n0, u.k0);
+      wg_tile<WIDE>(p, next_tile, u.n0, u.k0);
       u.kb0 = 0;
       u.kb1 = p.kblocks;
       u.slot = -1;
@@ -118,7 +138,7 @@ struct WgWalk {
     if (pos >= end) return false;
     const int t = wg_run_tile(p, pos);
     const long long base = static_cast<long long>(t) * p.kblocks;
-    wg_tile(p, p.whole_tiles + t, u.n0, u.k0);
+    wg_tile<WIDE>(p, p.whole_tiles + t, u.n0, u.k0);
     u.kb0 = static_cast<int>(pos - base);
     u.kb1 = static_cast<int>(min(end - base, static_cast<long long>(p.kblocks)));
     u.slot = (u.kb0 == 0 && u.kb1 == p.kblocks) ? -1 : 2 * w + (first ? 0 : 1);
@@ -219,16 +239,25 @@ __device__ __forceinline__ void wg_timeout(unsigned int* status, volatile int* a
   atomicOr(status, kTimeout);
 }
 
-template <typename G>
+// Arrive on the leader's barrier for shared memory that this warp has written
+// and passed to the async proxy.  Release at CTA scope: what the leader's
+// product reads are this CTA's own shared-memory writes, in place before the
+// arrival is sent.  A release at cluster scope would also wait for the
+// thread's accesses to global memory, 0.6 us a stage.
+__device__ __forceinline__ void arrive_leader(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <typename G, bool WIDE>
 __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __grid_constant__ WeightGradTc p) {
+  using C = WgCfg<WIDE>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + WG_BAR_OFF);   // leader's: both CTAs' dy
-  uint64_t* full_q = full_a + WG_STAGES;                               // this CTA's codes
-  uint64_t* ready = full_q + WG_STAGES;                                // this CTA's restored x
-  uint64_t* peer_ready = ready + WG_STAGES;                            // leader's: the other CTA's
-  uint64_t* empty = peer_ready + WG_STAGES;
-  uint64_t* tfull = empty + WG_STAGES;                                 // accumulator complete
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);   // leader's: both CTAs' dy
+  uint64_t* full_q = full_a + C::STAGES;                               // this CTA's codes
+  uint64_t* ready = full_q + C::STAGES;                                // leader's: both CTAs' restored x
+  uint64_t* empty = ready + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;                                 // accumulator complete
   uint64_t* tempty = tfull + 1;                                        // leader's: both CTAs' drained
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -237,11 +266,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   const int rank = static_cast<int>(sm100::cluster_ctarank());
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < WG_STAGES; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       sm100::mbar_init(&full_a[s], 1);
       sm100::mbar_init(&full_q[s], 1);
-      sm100::mbar_init(&ready[s], WG_WARPS);
-      sm100::mbar_init(&peer_ready[s], 1);
+      sm100::mbar_init(&ready[s], 2 * C::GROUP_WARPS);
       sm100::mbar_init(&empty[s], 1);
     }
     sm100::mbar_init(tfull, 1);
@@ -252,7 +280,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     sm100::prefetch_tmap(&p.tm_q);
   }
   if (warp == 1) {
-    sm100::tmem_alloc_pair(tmem_slot, WG_TMEM);
+    sm100::tmem_alloc_pair(tmem_slot, C::TMEM);
     sm100::tmem_relinquish_pair();
   }
   sm100::tc_fence_before();
@@ -264,7 +292,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   // a wait that gives up does so seconds after this
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
-  WgWalk walk(p);
+  WgWalk<WIDE> walk(p);
   WgUnit u;
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer
@@ -273,8 +301,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
       while (ok && walk.next(p, u)) {
-        const int nact = u.n0 + 256 < p.n ? 2 : 1;   // halves of the tile with columns of dy
-        const int kcol = u.k0 + rank * 128;
+        const int nact = C::SUBS == 2 && u.n0 + 256 < p.n ? 2 : 1;   // halves of the tile with columns of dy
+        const int kcol = u.k0 + rank * C::CODES;
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!sm100::mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
             wg_timeout(p.status, abort_flag);
@@ -283,9 +311,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
           }
           const int plane = kb / p.row_blocks;
           const int t0 = (kb - plane * p.row_blocks) * WG_BK;
-          uint8_t* sa = smem + stage * WG_STAGE;
-          uint8_t* sq = sa + WG_A_BYTES + WG_B_BYTES;
-          sm100::mbar_arrive_expect_tx(&full_q[stage], WG_Q_BYTES);
+          uint8_t* sa = smem + stage * C::STAGE;
+          uint8_t* sq = sa + C::A_BYTES + C::B_BYTES;
+          sm100::mbar_arrive_expect_tx(&full_q[stage], C::Q_BYTES);
           if (rank == 0) sm100::mbar_arrive_expect_tx(&full_a[stage], 2 * nact * WG_SUB_BYTES);
           issued |= 1u << stage;
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -301,7 +329,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
               sm100::tma_load_3d_pair(dst + WG_CHUNK, &p.tm_dy, bar, col + 64, t0, plane);
             }
           }
-          if (++stage == WG_STAGES) {
+          if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -309,7 +337,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
       }
       if (!ok) {
         // let every load issued into this CTA's shared memory land before exit
-        for (int s = 0; s < WG_STAGES; ++s) {
+        for (int s = 0; s < C::STAGES; ++s) {
           if (!((issued >> s) & 1u)) continue;
           const uint64_t t = sm100::globaltimer();
           while ((!sm100::mbar_try_wait(&full_q[s], (issued_phase >> s) & 1u) ||
@@ -322,12 +350,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = sm100::make_idesc_bf16(256, 256, 1, 1);
+      constexpr uint32_t idesc = sm100::make_idesc_bf16(256, C::TK, 1, 1);
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       while (ok && walk.next(p, u)) {
-        const int nact = u.n0 + 256 < p.n ? 2 : 1;
+        const int nact = C::SUBS == 2 && u.n0 + 256 < p.n ? 2 : 1;
         if (!sm100::mbar_wait(tempty, acc_phase ^ 1u, abort_flag)) {
           wg_timeout(p.status, abort_flag);
           break;
@@ -335,27 +363,26 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
         sm100::tc_fence_after();
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!sm100::mbar_wait(&full_a[stage], phase, abort_flag) ||
-              !sm100::mbar_wait(&ready[stage], phase, abort_flag) ||
-              !sm100::mbar_wait(&peer_ready[stage], phase, abort_flag)) {
+              !sm100::mbar_wait(&ready[stage], phase, abort_flag)) {
             wg_timeout(p.status, abort_flag);
             ok = false;
             break;
           }
           sm100::tc_fence_after();
-          const uint32_t sa = sm100::smem_u32(smem + stage * WG_STAGE);
+          const uint32_t sa = sm100::smem_u32(smem + stage * C::STAGE);
           const uint64_t ad = sm100::make_sdesc(sa, WG_CHUNK, 1024);
-          const uint64_t bd = sm100::make_sdesc(sa + WG_A_BYTES, WG_CHUNK, 1024);
+          const uint64_t bd = sm100::make_sdesc(sa + C::A_BYTES, WG_CHUNK, 1024);
 #pragma unroll
           for (int kk = 0; kk < WG_BK / 16; ++kk)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < C::SUBS; ++h)
               if (h < nact)
-                sm100::umma_bf16_pair(tmem + static_cast<uint32_t>(h * 256),
+                sm100::umma_bf16_pair(tmem + static_cast<uint32_t>(h * C::TK),
                                       ad + static_cast<uint64_t>((h * WG_SUB_BYTES + kk * 2048) >> 4),
                                       bd + static_cast<uint64_t>((kk * 2048) >> 4), idesc,
                                       (kb > u.kb0 || kk) ? 1u : 0u);
           sm100::umma_commit_pair_both(&empty[stage]);
-          if (++stage == WG_STAGES) {
+          if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -364,76 +391,76 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
         sm100::umma_commit_pair_both(tfull);
         acc_phase ^= 1u;
       }
-    } else if (lane == 0) {
-      // The other CTA's issuer relays its restored stages to the leader.  (An
-      // arrival on another CTA's barrier releases at cluster scope, which
-      // waits for the thread's loads in flight too: sent by the restoring
-      // warps themselves it made every stage wait for their exponents.)
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      while (ok && walk.next(p, u)) {
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (!sm100::mbar_wait(&ready[stage], phase, abort_flag)) {
-            wg_timeout(p.status, abort_flag);
-            ok = false;
-            break;
-          }
-          sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_u32(&peer_ready[stage]), 0));
-          if (++stage == WG_STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
     }
   } else {
     // ---------------------------------------- codes to bf16, then the tile
-    // thread j restores codes 16 (j % 8) .. + 15 of row j / 8 of every stage
-    const int j = threadIdx.x - 64;
-    const int f = j & 7, t = j >> 3;
-    // their place: chunk f / 4, units 2 (f % 4) and the next; the upper chunk's
-    // lanes write their two units in the other order, so that the 8 lanes of a
-    // row touch 8 different 16-byte columns at a time
+    // thread j of a group restores codes 16 (j % ROW_TASKS) .. + 15 of row
+    // j / ROW_TASKS of the group's stages
+    const int group = (warp - 2) / C::GROUP_WARPS;
+    const int j = threadIdx.x - 64 - group * C::GROUP_WARPS * 32;
+    const int f = j % C::ROW_TASKS, t = j / C::ROW_TASKS;
+    // Their place: chunk f / 4, units 2 (f % 4) and the next.  Where 8 lanes
+    // share a row, the upper chunk's write their two units in the other order,
+    // so that 8 neighbouring lanes always touch 8 different 16-byte columns
+    // (where 4 do, the swizzle of the two rows sees to it).
     const int swap = f >> 2;
-    const uint32_t src = WG_A_BYTES + WG_B_BYTES + t * 128 + f * 16;
-    const uint32_t dst = WG_A_BYTES + (f >> 2) * WG_CHUNK + t * 128;
+    const uint32_t src = C::A_BYTES + C::B_BYTES + t * C::CODES + f * 16;
+    const uint32_t dst = C::A_BYTES + (f >> 2) * WG_CHUNK + t * 128;
     const uint32_t dst0 = dst + ((((f & 3) * 2 + swap) ^ (t & 7)) << 4);
     const uint32_t dst1 = dst + ((((f & 3) * 2 + 1 - swap) ^ (t & 7)) << 4);
+    const uint32_t ready0 = sm100::mapa_shared(sm100::smem_u32(ready), 0);
     const uint32_t tempty0 = sm100::mapa_shared(sm100::smem_u32(tempty), 0);
     const int quad = warp & 3, slice = (warp - 2) >> 2;
+    constexpr int CH = C::TK / 32;
     const bool vec = (static_cast<long long>(p.k) * sizeof(G)) % 16 == 0;   // grad is 16-byte aligned
-    int stage = 0;
+    int stage = 0, turn = 0;   // ring position of the unit's first stage, and whose it is
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     while (ok && walk.next(p, u)) {
-      const int blk = (u.k0 >> 7) + rank;
-      // Exponents in the order of the unit's row blocks; 127 (any finite one)
-      // where the tensor map loads zeros.  Read four stages at a time, four
-      // ahead: a register that a load is still filling must not be touched, a
-      // copy included, or every stage waits out the load (1.3 us a stage
-      // with a two-deep shift register, at any amount of work per stage).
-      int tb = u.kb0 % p.row_blocks;
+      const int blk = (u.k0 + rank * C::CODES) / kCkptBlock;
+      // Exponents of the group's stages in the order of the unit's row blocks;
+      // 127 (any finite one) where the tensor map loads zeros.  Read four
+      // stages at a time, four ahead: a register that a load is still filling
+      // must not be touched, a copy included, or the stage waits out the load.
+      const int lead = (group + C::GROUPS - turn) % C::GROUPS;   // the group's first stage of the unit
+      int tb = (u.kb0 + lead) % p.row_blocks;
       auto exponent = [&]() -> int {
         const long long row = static_cast<long long>(tb) * WG_BK + t;
-        if (++tb == p.row_blocks) tb = 0;
+        tb += C::GROUPS;
+        while (tb >= p.row_blocks) tb -= p.row_blocks;
         return (row < p.rows && blk < p.nblk) ? p.exps[row * p.nblk + blk] : 127;
       };
       int e[4], e_next[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) e[i] = exponent();
-      for (int kb4 = u.kb0; ok && kb4 < u.kb1; kb4 += 4) {
+      auto advance = [&](int by) {   // by <= STAGES
+        stage += by;
+        if (stage >= C::STAGES) {
+          stage -= C::STAGES;
+          phase ^= 1u;
+        }
+      };
+      auto retreat = [&](int by) {
+        stage -= by;
+        if (stage < 0) {
+          stage += C::STAGES;
+          phase ^= 1u;
+        }
+      };
+      advance(lead);
+      int kb = u.kb0 + lead;
+      for (; ok && kb < u.kb1;) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) e_next[i] = exponent();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (kb4 + i >= u.kb1) break;
+          if (kb >= u.kb1) break;
           if (!__all_sync(0xffffffffu, sm100::mbar_wait(&full_q[stage], phase, abort_flag))) {
             if (lane == 0) wg_timeout(p.status, abort_flag);
             ok = false;
             break;
           }
-          uint8_t* base = smem + stage * WG_STAGE;
+          uint8_t* base = smem + stage * C::STAGE;
           const uint4 q = *reinterpret_cast<const uint4*>(base + src);
           uint4 lo, hi;
           restore16(q, e[i], lo, hi);
@@ -441,15 +468,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
           *reinterpret_cast<uint4*>(base + dst1) = swap ? lo : hi;
           sm100::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) sm100::mbar_arrive(&ready[stage]);
-          if (++stage == WG_STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (lane == 0) arrive_leader(ready0 + stage * 8);
+          advance(C::GROUPS);
+          kb += C::GROUPS;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = e_next[i];
       }
+      // kb is the group's first stage past the unit: back to the unit's end
+      retreat(kb - u.kb1);
+      turn = (turn + (u.kb1 - u.kb0)) % C::GROUPS;
       if (!ok) break;
       if (!__all_sync(0xffffffffu, sm100::mbar_wait(tfull, acc_phase, abort_flag))) {
         if (lane == 0) wg_timeout(p.status, abort_flag);
@@ -457,10 +485,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
       }
       sm100::tc_fence_after();
       acc_phase ^= 1u;
-      const int nact = u.n0 + 256 < p.n ? 2 : 1;
+      const int nact = C::SUBS == 2 && u.n0 + 256 < p.n ? 2 : 1;
 #pragma unroll 1
-      for (int c = slice; c < 8 * nact; c += 4) {   // 32-column chunks of the 512 accumulator columns
-        const int col = u.k0 + (c & 7) * 32;
+      for (int c = slice; c < CH * nact; c += 4) {   // 32-column chunks of the accumulator columns
+        const int col = u.k0 + (c % CH) * 32;
         if (col >= p.k) continue;
         uint32_t r[32];
         sm100::tmem_ld32_async(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c * 32), r);
@@ -470,14 +498,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
         for (int k = 0; k < 32; ++k)   // features 1 and 2 of every four back in place
           v[k >> 3][k & 7] = __uint_as_float(r[(k & 3) == 1 ? k + 1 : (k & 3) == 2 ? k - 1 : k]);
         transpose_pieces(v, lane);
-        const int row0 = u.n0 + (c >> 3) * 256 + rank * 128 + quad * 32 + (lane & ~3);
+        const int row0 = u.n0 + (c / CH) * 256 + rank * 128 + quad * 32 + (lane & ~3);
         const int c0 = col + (lane & 3) * 8;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = row0 + i;
           if (row >= p.n) continue;
           if (u.slot >= 0)
-            store_sector(p.partial + (static_cast<long long>(u.slot) * kWgTileN + (row - u.n0)) * kWgTileK + (c0 - u.k0), v[i]);
+            store_sector(p.partial + (static_cast<long long>(u.slot) * C::TN + (row - u.n0)) * C::TK + (c0 - u.k0), v[i]);
           else
             store_piece(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + c0, v[i], p.k - c0,
                         p.accumulate != 0, vec && c0 + 8 <= p.k);
@@ -496,15 +524,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   pdl_launch_dependents();
   if (warp == 1) {
     __syncwarp();
-    sm100::tmem_dealloc_pair(tmem, WG_TMEM);
+    sm100::tmem_dealloc_pair(tmem, C::TMEM);
   }
 }
 
 // grad (+)= the runs' sums of each tile that several workers share, in the
 // order of their rows.  Block (b, y): the tile that the start of worker b + 1's
-// run lies inside, if it is the first start inside it; rows 4 y .. 4 y + 3.
-template <typename G>
+// run lies inside, if it is the first start inside it; 1024 elements.
+template <typename G, bool WIDE>
 __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_constant__ WeightGradTc p) {
+  using C = WgCfg<WIDE>;
   pdl_launch_dependents();
   pdl_wait();
   const int w1 = blockIdx.x + 1;
@@ -513,8 +542,9 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
   const long long t0 = static_cast<long long>(t) * p.kblocks, t1 = t0 + p.kblocks;
   if (at == t0 || wg_run(p, w1 - 1) > t0) return;
   int n0, k0;
-  wg_tile(p, p.whole_tiles + t, n0, k0);
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 6), c = (threadIdx.x & 63) * 4;
+  wg_tile<WIDE>(p, p.whole_tiles + t, n0, k0);
+  constexpr int QUADS = C::TK / 4;   // threads per row
+  const int r = blockIdx.y * (256 / QUADS) + threadIdx.x / QUADS, c = (threadIdx.x % QUADS) * 4;
   const int row = n0 + r, col = k0 + c;
   if (row >= p.n || col >= p.k) return;
   float s[4] = {};
@@ -524,7 +554,7 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
   for (int w = w1 - 1; w < w_end; ++w) {
     const int slot = 2 * w + (wg_run(p, w) >= t0 ? 0 : 1);   // 0: the tile its run starts in
     const float4 v = *reinterpret_cast<const float4*>(
-        p.partial + (static_cast<long long>(slot) * kWgTileN + r) * kWgTileK + c);
+        p.partial + (static_cast<long long>(slot) * C::TN + r) * C::TK + c);
     s[0] += v.x;
     s[1] += v.y;
     s[2] += v.z;
@@ -580,14 +610,14 @@ __global__ void __launch_bounds__(256) weight_grad_stage_kernel(const D* dy, lon
 }
 
 // ---------------------------------------------------------------- launchers
-template <typename G>
+template <typename G, bool WIDE>
 static cudaError_t tc_launch(const WeightGradTc& p, cudaStream_t s) {
-  auto kern = weight_grad_tc_kernel<G>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WG_SMEM);
+  auto kern = weight_grad_tc_kernel<G, WIDE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WgCfg<WIDE>::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(WG_THREADS);
-  cfg.dynamicSmemBytes = WG_SMEM;
+  cfg.dynamicSmemBytes = WgCfg<WIDE>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -601,14 +631,20 @@ static cudaError_t tc_launch(const WeightGradTc& p, cudaStream_t s) {
   cfg.gridDim = dim3(2 * p.workers);
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
-cudaError_t launch_weight_grad_tc(const WeightGradTc& p, cudaStream_t s) {
-  return p.grad_bf16 ? tc_launch<__nv_bfloat16>(p, s) : tc_launch<float>(p, s);
+template <typename G, bool WIDE>
+static cudaError_t join_launch(const WeightGradTc& p, cudaStream_t s) {
+  const dim3 grid(p.workers - 1, WgCfg<WIDE>::TN * WgCfg<WIDE>::TK / 1024);
+  return launch_pdl(weight_grad_join_kernel<G, WIDE>, grid, dim3(256), 0, s, p);
 }
-
+cudaError_t launch_weight_grad_tc(const WeightGradTc& p, cudaStream_t s) {
+  using B = __nv_bfloat16;
+  if (p.wide) return p.grad_bf16 ? tc_launch<B, true>(p, s) : tc_launch<float, true>(p, s);
+  return p.grad_bf16 ? tc_launch<B, false>(p, s) : tc_launch<float, false>(p, s);
+}
 cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s) {
-  const dim3 grid(p.workers - 1, kWgTileN / 4);
-  return p.grad_bf16 ? launch_pdl(weight_grad_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p)
-                     : launch_pdl(weight_grad_join_kernel<float>, grid, dim3(256), 0, s, p);
+  using B = __nv_bfloat16;
+  if (p.wide) return p.grad_bf16 ? join_launch<B, true>(p, s) : join_launch<float, true>(p, s);
+  return p.grad_bf16 ? join_launch<B, false>(p, s) : join_launch<float, false>(p, s);
 }
 
 cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,
