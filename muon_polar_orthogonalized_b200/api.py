@@ -16,6 +16,8 @@ import ctypes
 from ctypes import c_double, c_float, c_int64, c_void_p
 from typing import List, Optional, Sequence, Tuple
 
+import torch
+
 from . import _native as N
 from ._native import AdamWGroup, MuonGroup, check
 
@@ -23,7 +25,6 @@ GroupSpec = Tuple[int, int, int, int, int, float]  # rows, cols, count, first, g
 
 
 def _stream_handle(stream) -> int:
-    import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
 
@@ -43,7 +44,6 @@ def _group_fields(s) -> Tuple[int, int, int, int, int]:
 
 
 def _torch_dtype(code: int):
-    import torch
     return torch.bfloat16 if code == N.MUON_BF16 else torch.float32
 
 
@@ -71,7 +71,6 @@ def _check_group_lists(groups: Sequence, lists) -> None:
 
 
 def _check_step_args(groups, params, grads, momentum) -> None:
-    import torch
     _check_group_lists(groups, (("params", params, torch.float32), ("grads", grads, None),
                                 ("momentum", momentum, torch.float32)))
 
@@ -137,7 +136,6 @@ def muon_step_replicated(params, grads, momentum, groups: Sequence, lr: float, b
     """muon_step that also writes each updated matrix into every replica list
     (replicas[r][i] is copy r of params[i]; tensors or raw device pointers,
     possibly in peer GPUs' memory)."""
-    import torch
     _check_step_args(groups, params, grads, momentum)
     for r, rep in enumerate(replicas):
         _check_group_lists(groups, ((f"replicas[{r}]", rep, torch.float32),))
@@ -157,7 +155,6 @@ def muon_step_replicated(params, grads, momentum, groups: Sequence, lr: float, b
 def muon_reduce_mean(dst: Sequence, sources: Sequence[Sequence], stream=None) -> None:
     """dst[i] <- mean over r of sources[r][i] (fp32 or bf16 tensors of one
     dtype; sources may live in peer GPUs' memory)."""
-    import torch
     if not dst:
         return
     if dst[0].dtype not in (torch.float32, torch.bfloat16):
@@ -200,7 +197,6 @@ def muon_step_scheduled(params, grads, momentum, groups: Sequence, lr: float, be
 def new_schedule_state(device, lr_mult: float = 1.0, step: int = 0):
     """A device-resident schedule state {float lr_mult; float reserved; int64 step}."""
     import struct
-    import torch
     raw = struct.pack("<ffq", float(lr_mult), 0.0, int(step))
     return torch.frombuffer(bytearray(raw), dtype=torch.uint8).to(device)
 
@@ -229,7 +225,6 @@ def muon_schedule_advance_cosine(schedule_state, total_steps: int, warmup_steps:
 
 def muon_orthogonalize(inputs, outputs, groups: Sequence, ns_steps: int, coeffs, flags: int,
                        workspace, workspace_bytes: Optional[int] = None, stream=None) -> None:
-    import torch
     _check_group_lists(groups, (("inputs", inputs, None), ("outputs", outputs, torch.float32)))
     g = make_groups(groups)
     ca = _coeff_array(coeffs, ns_steps)
@@ -248,8 +243,7 @@ class AdamWSpec:
         self.params, self.grads, self.exp_avg, self.exp_avg_sq = params, grads, exp_avg, exp_avg_sq
         self.lr, self.beta1, self.beta2, self.eps, self.wd = lr, beta1, beta2, eps, wd
         if grad_dtype is None:
-            import torch
-            grad_dtype = N.MUON_BF16 if (grads and grads[0].dtype == torch.bfloat16) else N.MUON_F32
+                    grad_dtype = N.MUON_BF16 if (grads and grads[0].dtype == torch.bfloat16) else N.MUON_F32
         self.grad_dtype = grad_dtype
 
 
@@ -257,7 +251,6 @@ def _adamw_groups(groups: Sequence[AdamWSpec]):
     n = len(groups)
     arr = (AdamWGroup * max(n, 1))()
     keep = []
-    import torch
     for i, g in enumerate(groups):
         n_t = len(g.params)
         for name in ("grads", "exp_avg", "exp_avg_sq"):
@@ -296,51 +289,79 @@ def adamw_step_scheduled(groups: Sequence[AdamWSpec], schedule_state, stream=Non
 
 
 # ------------------------------------------- operators that make the gradients
-def _on_device(fn: str, tensors, stream):
-    """(device context, stream handle) of a call whose tensors must share one
-    CUDA device; the stream defaults to that device's current one."""
-    import torch
-    dev = None
-    for name, t in tensors:
+# These run many times a step, some for a few microseconds, so their checks are
+# kept short: one device index per tensor, no device switch where the tensors'
+# device is the current one, shapes walked only where a tensor is strided.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _device_of(fn: str, *tensors) -> int:
+    """The one CUDA device of (name, tensor) pairs given flat; None is skipped."""
+    dev = -1
+    for i in range(1, len(tensors), 2):
+        t = tensors[i]
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: {name} is not a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{fn}: {name} is on {t.device}, the others on {dev}")
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"{fn}: stream of {s.device}, tensors on {dev}")
-    return torch.cuda.device(dev), c_void_p(int(s.cuda_stream))
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{fn}: {tensors[i - 1]} is not a CUDA tensor")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{fn}: {tensors[i - 1]} is on cuda:{d}, {tensors[0]} on cuda:{dev}")
+    return dev
+
+
+def _launch(fn: str, dev: int, stream, call, *args) -> None:
+    """call(*args, stream) with the tensors' device current, on `stream` or
+    that device's current stream."""
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"{fn}: stream of {stream.device}, tensors on cuda:{dev}")
+    else:
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = call(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, handle)
+    if st != N.MUON_OK:
+        check(st, fn)
 
 
 def _dtype_code(fn: str, name: str, t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return N.MUON_F32
-    if t.dtype == torch.bfloat16:
+    d = t.dtype
+    if d is torch.bfloat16:
         return N.MUON_BF16
-    raise ValueError(f"{fn}: {name} must be fp32 or bf16, got {t.dtype}")
+    if d is torch.float32:
+        return N.MUON_F32
+    raise ValueError(f"{fn}: {name} must be fp32 or bf16, got {d}")
 
 
 def _rows(fn: str, name: str, t, cols: Optional[int] = None, rows: Optional[int] = None):
     """(rows, columns, pitch) of an activation tensor [..., columns]: rows of
     adjacent elements a constant pitch apart."""
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{fn}: {name} has no dimension")
-    c = t.shape[-1]
-    r = 1
-    for d in t.shape[:-1]:
-        r *= d
+    c = shape[-1]
+    if len(shape) == 2:
+        r = shape[0]
+    else:
+        r = 1
+        for d in shape[:-1]:
+            r *= d
     if (cols is not None and c != cols) or (rows is not None and r != rows):
-        raise ValueError(f"{fn}: {name} {tuple(t.shape)} is not {'*' if rows is None else rows} rows of "
+        raise ValueError(f"{fn}: {name} {tuple(shape)} is not {'*' if rows is None else rows} rows of "
                          f"{'*' if cols is None else cols}")
+    if t.is_contiguous():
+        return r, c, c
     if c > 1 and t.stride(-1) != 1:
         raise ValueError(f"{fn}: the elements of a row of {name} are not adjacent")
     pitch, span = None, 1   # leading dimensions, innermost first, must step evenly through the rows
-    for size, stride in list(zip(t.shape[:-1], t.stride()[:-1]))[::-1]:
+    for size, stride in list(zip(shape[:-1], t.stride()[:-1]))[::-1]:
         if size == 1:
             continue
         if pitch is None:
@@ -355,21 +376,31 @@ def _rows(fn: str, name: str, t, cols: Optional[int] = None, rows: Optional[int]
     return r, c, pitch
 
 
-def _dense(fn: str, name: str, t, shape, dtype=None) -> None:
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{fn}: {name} must be a contiguous{'' if dtype is None else f' {dtype}'} tensor of shape "
-                         f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+def _dense(fn: str, name: str, t, numel: int, last: int, dtype=None) -> None:
+    """A contiguous tensor of numel elements, rows of `last`."""
+    if t.numel() != numel or t.shape[-1:] != (last,) or not t.is_contiguous() or \
+            (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{fn}: {name} must be contiguous{'' if dtype is None else f' {dtype}'}, {numel} elements in "
+                         f"rows of {last}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _row_values(fn: str, name: str, t, rows: int) -> None:
+    if t.numel() != rows or t.dtype is not torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous fp32, one value for each of {rows} rows, got {t.dtype} "
+                         f"{tuple(t.shape)}")
 
 
 def _ids(fn: str, ids):
-    import torch
-    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+    d = ids.dtype
+    if (d is not torch.int64 and d is not torch.int32) or not ids.is_contiguous():
         raise ValueError(f"{fn}: ids must be a contiguous int32 or int64 tensor")
-    return (32 if ids.dtype == torch.int32 else 64), ids.numel()
+    return (64 if d is torch.int64 else 32), ids.numel()
 
 
-def _ptr(t) -> c_void_p:
-    return c_void_p(0 if t is None else t.data_ptr())
+def _table(fn: str, name: str, t):
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous [vocab, dim] tensor, got {tuple(t.shape)}")
+    return t.shape
 
 
 def _workspace(fn: str, ws) -> int:
@@ -383,17 +414,12 @@ def muon_embedding_forward(table, ids, out, scale: float = 1.0, stream=None) -> 
     [0, vocab).  table: fp32 or bf16 [vocab, dim]; ids: int32 or int64, any
     shape; out: fp32 or bf16 [*ids.shape, dim] (rows may be strided)."""
     fn = "muon_embedding_forward"
-    ctx, s = _on_device(fn, (("table", table), ("ids", ids), ("out", out)), stream)
-    if table.dim() != 2:
-        raise ValueError(f"{fn}: table must be [vocab, dim]")
-    vocab, dim = table.shape
-    _dense(fn, "table", table, (vocab, dim))
+    dev = _device_of(fn, "table", table, "ids", ids, "out", out)
+    vocab, dim = _table(fn, "table", table)
     bits, n = _ids(fn, ids)
     _, _, pitch = _rows(fn, "out", out, dim, n)
-    with ctx:
-        st = N.lib().muon_embedding_forward(_ptr(table), _dtype_code(fn, "table", table), vocab, dim, _ptr(ids), bits,
-                                            n, float(scale), _ptr(out), _dtype_code(fn, "out", out), pitch, s)
-    check(st, fn)
+    _launch(fn, dev, stream, N.lib().muon_embedding_forward, table.data_ptr(), _dtype_code(fn, "table", table), vocab,
+            dim, ids.data_ptr(), bits, n, scale, out.data_ptr(), _dtype_code(fn, "out", out), pitch)
 
 
 def muon_embedding_grad_workspace_size(vocab: int, dim: int, n: int) -> int:
@@ -405,40 +431,31 @@ def muon_embedding_grad(dout, ids, grad, workspace, scale: float = 1.0, accumula
     """grad[v] <- (grad[v] +) scale * sum of dout[t] over t with ids[t] = v.
     dout: fp32 or bf16 [*ids.shape, dim]; grad: fp32 or bf16 [vocab, dim]."""
     fn = "muon_embedding_grad"
-    ctx, s = _on_device(fn, (("dout", dout), ("ids", ids), ("grad", grad), ("workspace", workspace)), stream)
-    if grad.dim() != 2:
-        raise ValueError(f"{fn}: grad must be [vocab, dim]")
-    vocab, dim = grad.shape
-    _dense(fn, "grad", grad, (vocab, dim))
+    dev = _device_of(fn, "dout", dout, "ids", ids, "grad", grad, "workspace", workspace)
+    vocab, dim = _table(fn, "grad", grad)
     bits, n = _ids(fn, ids)
     _, _, pitch = _rows(fn, "dout", dout, dim, n)
-    with ctx:
-        st = N.lib().muon_embedding_grad(_ptr(dout), _dtype_code(fn, "dout", dout), pitch, _ptr(ids), bits, n, vocab,
-                                         dim, float(scale), _ptr(grad), _dtype_code(fn, "grad", grad),
-                                         1 if accumulate else 0, _ptr(workspace), _workspace(fn, workspace), s)
-    check(st, fn)
+    _launch(fn, dev, stream, N.lib().muon_embedding_grad, dout.data_ptr(), _dtype_code(fn, "dout", dout), pitch,
+            ids.data_ptr(), bits, n, vocab, dim, scale, grad.data_ptr(), _dtype_code(fn, "grad", grad),
+            1 if accumulate else 0, workspace.data_ptr(), _workspace(fn, workspace))
 
 
 def muon_layer_norm_forward(x, gain, bias, y, mean, rstd, eps: float = 1e-5, stream=None) -> None:
     """y <- (x - mean) * rstd * gain + bias over the last dimension; mean and
     rstd (fp32, one per row) are written for the backward pass.  x, y: fp32 or
     bf16; gain, bias: fp32 [cols] (bias may be None)."""
-    import torch
     fn = "muon_layer_norm_forward"
-    ctx, s = _on_device(fn, (("x", x), ("gain", gain), ("bias", bias), ("y", y), ("mean", mean), ("rstd", rstd)),
-                        stream)
+    dev = _device_of(fn, "x", x, "gain", gain, "bias", bias, "y", y, "mean", mean, "rstd", rstd)
     rows, cols, xp = _rows(fn, "x", x)
     _, _, yp = _rows(fn, "y", y, cols, rows)
-    _dense(fn, "gain", gain, (cols,), torch.float32)
+    _dense(fn, "gain", gain, cols, cols, torch.float32)
     if bias is not None:
-        _dense(fn, "bias", bias, (cols,), torch.float32)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _dense(fn, name, t.view(-1) if t.is_contiguous() else t, (rows,), torch.float32)
-    with ctx:
-        st = N.lib().muon_layer_norm_forward(_ptr(x), _dtype_code(fn, "x", x), xp, rows, cols, _ptr(gain), _ptr(bias),
-                                             float(eps), _ptr(y), _dtype_code(fn, "y", y), yp, _ptr(mean), _ptr(rstd),
-                                             s)
-    check(st, fn)
+        _dense(fn, "bias", bias, cols, cols, torch.float32)
+    _row_values(fn, "mean", mean, rows)
+    _row_values(fn, "rstd", rstd, rows)
+    _launch(fn, dev, stream, N.lib().muon_layer_norm_forward, x.data_ptr(), _dtype_code(fn, "x", x), xp, rows, cols,
+            gain.data_ptr(), None if bias is None else bias.data_ptr(), eps, y.data_ptr(), _dtype_code(fn, "y", y), yp,
+            mean.data_ptr(), rstd.data_ptr())
 
 
 def muon_layer_norm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -450,27 +467,24 @@ def muon_layer_norm_backward(dy, x, gain, mean, rstd, dx, dgain, dbias, workspac
     """The gradients of muon_layer_norm_forward: dx (the type of x and dy),
     and dgain and dbias (fp32 or bf16 [cols]; dbias may be None), overwritten
     or added to."""
-    import torch
     fn = "muon_layer_norm_backward"
-    ctx, s = _on_device(fn, (("dy", dy), ("x", x), ("gain", gain), ("mean", mean), ("rstd", rstd), ("dx", dx),
-                             ("dgain", dgain), ("dbias", dbias), ("workspace", workspace)), stream)
+    dev = _device_of(fn, "dy", dy, "x", x, "gain", gain, "mean", mean, "rstd", rstd, "dx", dx, "dgain", dgain,
+                     "dbias", dbias, "workspace", workspace)
     rows, cols, xp = _rows(fn, "x", x)
     _, _, dyp = _rows(fn, "dy", dy, cols, rows)
     _, _, dxp = _rows(fn, "dx", dx, cols, rows)
-    if not (dy.dtype == x.dtype == dx.dtype):
+    if not (dy.dtype is x.dtype and dx.dtype is x.dtype):
         raise ValueError(f"{fn}: dy, x and dx must have one type, got {dy.dtype}, {x.dtype}, {dx.dtype}")
-    _dense(fn, "gain", gain, (cols,), torch.float32)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _dense(fn, name, t.view(-1) if t.is_contiguous() else t, (rows,), torch.float32)
-    _dense(fn, "dgain", dgain, (cols,))
+    _dense(fn, "gain", gain, cols, cols, torch.float32)
+    _row_values(fn, "mean", mean, rows)
+    _row_values(fn, "rstd", rstd, rows)
+    _dense(fn, "dgain", dgain, cols, cols)
     if dbias is not None:
-        _dense(fn, "dbias", dbias, (cols,), dgain.dtype)
-    with ctx:
-        st = N.lib().muon_layer_norm_backward(_ptr(dy), dyp, _ptr(x), _dtype_code(fn, "x", x), xp, rows, cols,
-                                              _ptr(gain), _ptr(mean), _ptr(rstd), _ptr(dx), dxp, _ptr(dgain),
-                                              _ptr(dbias), _dtype_code(fn, "dgain", dgain), 1 if accumulate else 0,
-                                              _ptr(workspace), _workspace(fn, workspace), s)
-    check(st, fn)
+        _dense(fn, "dbias", dbias, cols, cols, dgain.dtype)
+    _launch(fn, dev, stream, N.lib().muon_layer_norm_backward, dy.data_ptr(), dyp, x.data_ptr(),
+            _dtype_code(fn, "x", x), xp, rows, cols, gain.data_ptr(), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+            dxp, dgain.data_ptr(), None if dbias is None else dbias.data_ptr(), _dtype_code(fn, "dgain", dgain),
+            1 if accumulate else 0, workspace.data_ptr(), _workspace(fn, workspace))
 
 
 CHECKPOINT_BLOCK = 128   # features that share one exponent of a checkpoint
@@ -482,14 +496,14 @@ class Checkpoint:
     least cols), and exponents, uint8 [rows, ceil(cols / 128)]."""
 
     def __init__(self, codes, exponents, cols: int):
-        import torch
-        nb = (int(cols) + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
+        cols = int(cols)
+        nb = (cols + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
         if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.shape[1] < cols \
                 or codes.shape[1] % 16 != 0 or cols < 1:
             raise ValueError("Checkpoint: codes must be contiguous uint8 [rows, pitch], pitch a multiple of 16 and "
                              f"at least cols = {cols}, got {codes.dtype} {tuple(codes.shape)}")
-        _dense("Checkpoint", "exponents", exponents, (codes.shape[0], nb), torch.uint8)
-        self.codes, self.exponents, self.cols = codes, exponents, int(cols)
+        _dense("Checkpoint", "exponents", exponents, codes.shape[0] * nb, nb, torch.uint8)
+        self.codes, self.exponents, self.cols = codes, exponents, cols
 
     @property
     def rows(self) -> int:
@@ -498,7 +512,6 @@ class Checkpoint:
 
 def new_checkpoint(rows: int, cols: int, device) -> Checkpoint:
     """An uninitialised checkpoint for muon_checkpoint_pack to fill."""
-    import torch
     pitch = (int(cols) + 15) // 16 * 16
     nb = (int(cols) + CHECKPOINT_BLOCK - 1) // CHECKPOINT_BLOCK
     return Checkpoint(torch.empty(int(rows), pitch, dtype=torch.uint8, device=device),
@@ -508,30 +521,27 @@ def new_checkpoint(rows: int, cols: int, device) -> Checkpoint:
 def muon_checkpoint_pack(x, ckpt: Checkpoint, stream=None) -> None:
     """Fill ckpt from x, fp32 or bf16 [..., cols] (rows may be strided)."""
     fn = "muon_checkpoint_pack"
-    ctx, s = _on_device(fn, (("x", x), ("codes", ckpt.codes), ("exponents", ckpt.exponents)), stream)
-    rows, cols, pitch = _rows(fn, "x", x, ckpt.cols, ckpt.rows)
-    with ctx:
-        st = N.lib().muon_checkpoint_pack(_ptr(x), _dtype_code(fn, "x", x), pitch, rows, cols, _ptr(ckpt.codes),
-                                          ckpt.codes.shape[1], _ptr(ckpt.exponents), s)
-    check(st, fn)
+    codes, exps = ckpt.codes, ckpt.exponents
+    dev = _device_of(fn, "x", x, "codes", codes, "exponents", exps)
+    rows, cols, pitch = _rows(fn, "x", x, ckpt.cols, codes.shape[0])
+    _launch(fn, dev, stream, N.lib().muon_checkpoint_pack, x.data_ptr(), _dtype_code(fn, "x", x), pitch, rows, cols,
+            codes.data_ptr(), codes.shape[1], exps.data_ptr())
 
 
 def muon_checkpoint_unpack(ckpt: Checkpoint, out, stream=None) -> None:
     """out <- the values the checkpoint stands for (fp32 or bf16, both exact)."""
     fn = "muon_checkpoint_unpack"
-    ctx, s = _on_device(fn, (("codes", ckpt.codes), ("exponents", ckpt.exponents), ("out", out)), stream)
-    rows, cols, pitch = _rows(fn, "out", out, ckpt.cols, ckpt.rows)
-    with ctx:
-        st = N.lib().muon_checkpoint_unpack(_ptr(ckpt.codes), ckpt.codes.shape[1], _ptr(ckpt.exponents), rows, cols,
-                                            _ptr(out), _dtype_code(fn, "out", out), pitch, s)
-    check(st, fn)
+    codes, exps = ckpt.codes, ckpt.exponents
+    dev = _device_of(fn, "codes", codes, "exponents", exps, "out", out)
+    rows, cols, pitch = _rows(fn, "out", out, ckpt.cols, codes.shape[0])
+    _launch(fn, dev, stream, N.lib().muon_checkpoint_unpack, codes.data_ptr(), codes.shape[1], exps.data_ptr(), rows,
+            cols, out.data_ptr(), _dtype_code(fn, "out", out), pitch)
 
 
 def muon_checkpoint_weight_grad_workspace_size(rows: int, n: int, k: int, dy_dtype, dy_aligned: bool = True) -> int:
     """dy_dtype: torch.float32 or torch.bfloat16.  dy_aligned=False also counts
     the copy of a bf16 dy whose pointer or row pitch is not a multiple of 16
     bytes."""
-    import torch
     code = {torch.float32: N.MUON_F32, torch.bfloat16: N.MUON_BF16}.get(dy_dtype, -1)
     return int(N.lib().muon_checkpoint_weight_grad_workspace_size(int(rows), int(n), int(k), code,
                                                                    1 if dy_aligned else 0))
@@ -542,16 +552,13 @@ def muon_checkpoint_weight_grad(dy, ckpt: Checkpoint, grad, workspace, accumulat
     """grad [n, k] <- (grad +) dy^T x: the gradient of W [n, k] in y = x W^T from
     dy (fp32 or bf16 [..., n]) and the checkpoint of x [rows, k]."""
     fn = "muon_checkpoint_weight_grad"
-    ctx, s = _on_device(fn, (("dy", dy), ("codes", ckpt.codes), ("exponents", ckpt.exponents), ("grad", grad),
-                             ("workspace", workspace)), stream)
-    rows, n, pitch = _rows(fn, "dy", dy, None, ckpt.rows)
-    _dense(fn, "grad", grad, (n, ckpt.cols))
-    with ctx:
-        st = N.lib().muon_checkpoint_weight_grad(_ptr(dy), _dtype_code(fn, "dy", dy), pitch, rows, n,
-                                                 _ptr(ckpt.codes), ckpt.codes.shape[1], _ptr(ckpt.exponents),
-                                                 ckpt.cols, _ptr(grad), _dtype_code(fn, "grad", grad),
-                                                 1 if accumulate else 0, _ptr(workspace), _workspace(fn, workspace), s)
-    check(st, fn)
+    codes, exps = ckpt.codes, ckpt.exponents
+    dev = _device_of(fn, "dy", dy, "codes", codes, "exponents", exps, "grad", grad, "workspace", workspace)
+    rows, n, pitch = _rows(fn, "dy", dy, None, codes.shape[0])
+    _dense(fn, "grad", grad, n * ckpt.cols, ckpt.cols)
+    _launch(fn, dev, stream, N.lib().muon_checkpoint_weight_grad, dy.data_ptr(), _dtype_code(fn, "dy", dy), pitch, rows,
+            n, codes.data_ptr(), codes.shape[1], exps.data_ptr(), ckpt.cols, grad.data_ptr(),
+            _dtype_code(fn, "grad", grad), 1 if accumulate else 0, workspace.data_ptr(), _workspace(fn, workspace))
 
 
 def muon_query_status(workspace, stream=None) -> int:

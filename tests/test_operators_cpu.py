@@ -130,27 +130,14 @@ def test_workspace_sizes_refuse_and_grow(L):
 class OnGpu(torch.Tensor):
     """A CPU tensor that says it is on a GPU (nothing is launched with it)."""
 
-    @property
-    def is_cuda(self):
-        return True
+    def get_device(self):
+        return getattr(self, "on", 0)
 
 
-def fake(*shape, dtype=torch.float32):
-    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
-
-
-@pytest.fixture
-def no_stream(monkeypatch):
-    class S:
-        device, cuda_stream = torch.device("cpu"), 0
-
-        def __enter__(self):
-            return self
-
-        def __exit__(self, *a):
-            return False
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: S())
-    monkeypatch.setattr(torch.cuda, "device", lambda dev: S())
+def fake(*shape, dtype=torch.float32, on=0):
+    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+    t.on = on
+    return t
 
 
 def ids(n, dtype=torch.int64):
@@ -159,6 +146,7 @@ def ids(n, dtype=torch.int64):
 
 @pytest.mark.parametrize("match,call", [
     ("not a CUDA", lambda: api.muon_embedding_forward(torch.zeros(4, 8), ids(3), fake(3, 8))),
+    ("cuda:1", lambda: api.muon_embedding_forward(fake(4, 8), ids(3), fake(3, 8, on=1))),
     ("table", lambda: api.muon_embedding_forward(fake(4, 2, 4), ids(3), fake(3, 8))),
     ("table", lambda: api.muon_embedding_forward(fake(4, 16)[:, :8], ids(3), fake(3, 8))),
     ("table must be fp32 or bf16", lambda: api.muon_embedding_forward(fake(4, 8, dtype=torch.float16), ids(3), fake(3, 8))),
@@ -186,7 +174,7 @@ def ids(n, dtype=torch.int64):
     ("exponents", lambda: api.Checkpoint(torch.zeros(3, 144, dtype=torch.uint8), torch.zeros(3, 1, dtype=torch.uint8), 129)),
     ("not a CUDA", lambda: api.muon_checkpoint_pack(torch.zeros(3, 20), api.new_checkpoint(3, 20, "cpu"))),
 ])
-def test_binding_refuses(no_stream, match, call):
+def test_binding_refuses(match, call):
     with pytest.raises(ValueError, match=match):
         call()
 
