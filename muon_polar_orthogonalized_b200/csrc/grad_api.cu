@@ -302,6 +302,7 @@ muon_status muon_layer_norm_forward(const void* x, int32_t x_dtype, int64_t x_pi
     p.y_bf16 = y_dtype == MUON_BF16;
     p.vec = rows_vec(x, x_dtype, cols, x_pitch) && rows_vec(y, y_dtype, cols, y_pitch);
     p.eps = eps;
+    p.sms = sms;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return launched(api_timed_launch(K_LAYER_NORM, s, [&] { return launch_layer_norm(p, s); }), "layer norm launch");
   });
@@ -351,7 +352,8 @@ muon_status muon_layer_norm_backward(const void* dy, int64_t dy_pitch, const voi
     p.grad_bf16 = grad_dtype == MUON_BF16;
     p.accumulate = accumulate != 0;
     p.vec = rows_vec(x, dtype, cols, x_pitch) && rows_vec(dy, dtype, cols, dy_pitch) && rows_vec(dx, dtype, cols, dx_pitch);
-    p.blocks = layer_norm_grad_blocks(rows, p.cols, std::min(sms, 160));
+    p.sms = std::min(sms, 160);
+    p.blocks = layer_norm_grad_blocks(rows, p.cols, p.sms);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (rows > 0) {
       st = launched(api_timed_launch(K_LAYER_NORM_GRAD, s, [&] { return launch_layer_norm_grad(p, s); }),

@@ -57,6 +57,7 @@ struct NormParams {
   int x_bf16, y_bf16, grad_bf16, accumulate;
   int vec;
   int blocks;          // backward: persistent blocks
+  int sms;
   float eps;
 };
 

@@ -9,13 +9,21 @@
 // All sums are in fp32 and in an order that depends on the shape alone.  The
 // floor is HBM: x and y (forward), x, dy and dx (backward), once each.
 //
-// A row lives in the registers of one warp (up to 1024 columns) or of one
-// block, so x is read once and the variance is taken about the mean in a
-// second pass over registers (a one-pass sum of squares would cancel for rows
-// far from zero).  The backward kernel is persistent: a block walks rows
-// b, b + blocks, ... and keeps its columns' dgain and dbias sums on chip, then
-// writes one partial row per block; a second kernel adds the partial rows in
-// order.  The number of blocks depends on the shape and the SM count only.
+// A group of threads shares a row, 8 or 16 columns per thread, and the variance
+// is taken about the mean in a second pass over the row (a one-pass sum of
+// squares would cancel for rows far from zero).  Blocks are persistent, and
+// every thread copies its columns of the rows ahead into a ring of its own in
+// shared memory (cp.async): the next rows are in flight at no cost in registers
+// and with no barrier, since no thread reads another's copy, and each pass over
+// a row reads it from there again.  What bounds it then is the chain of a row's
+// two sums (exchange, barrier, exchange: about 1.2 us a row for the few groups
+// an SM holds), so a group takes R rows at a time and sums all of them in one
+// exchange.  Gain and bias stay in registers (read from L1 for every row, they
+// kept it 82% busy).  Backward, a thread keeps its columns' dgain and dbias sums
+// in registers; the block's groups are added in order into one partial row per
+// block, and a second kernel adds the partial rows in order.  Rows that 16-byte
+// accesses do not fit (odd widths) are loaded element by element, without the
+// ring.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,187 +33,389 @@
 
 namespace muon {
 
-// Sum over the threads of a row group (a warp, or the whole block), the same
-// bits in every thread.  `red` holds 2 x 32 floats, used alternately so that
-// one barrier per sum suffices.
-template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&s)[N], float* red, int& flip) {
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* r = red + flip * N * 32;
-    flip ^= 1;
-    if (lane == 0)
-#pragma unroll
-      for (int n = 0; n < N; ++n) r[n * 32 + warp] = s[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float t = lane < W ? r[n * 32 + lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      s[n] = t;
-    }
-  }
-}
+constexpr int kNormThreads = 256;   // of a block that holds several groups
 
-// A thread's share of a row: ITEMS units of 8 adjacent columns (VEC), or
-// ITEMS * 8 single columns; neighbouring threads hold neighbouring units.
-template <int TPR, bool VEC>
-struct Share {
-  // column of element e (0..7) of unit i for thread `t` of the row group
-  static __device__ __forceinline__ int col(int t, int i, int e) {
-    return VEC ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
+// Where a row's columns live: blockDim.x threads (a multiple of 32) per group,
+// blockDim.y groups.  Unit i of thread t is 8 adjacent columns (VEC) or 8 that
+// lie blockDim.x apart.
+template <bool VEC>
+struct Cols {
+  static __device__ __forceinline__ int at(int i, int e) {
+    const int t = threadIdx.x, n = blockDim.x;
+    return VEC ? (i * n + t) * 8 + e : (i * 8 + e) * n + t;
   }
+  // whether a unit holds any of the row's columns (VEC: then all 8)
+  static __device__ __forceinline__ bool inside(int i, int cols) { return at(i, 0) < cols; }
+  // units that are inside only; scalar columns past the row load as zeros
   template <typename T>
-  static __device__ __forceinline__ void load(const T* row, int t, int i, int cols, float (&v)[8]) {
+  static __device__ __forceinline__ void load(const T* row, int i, int cols, float2 (&v)[4]) {
     if constexpr (VEC) {
-      if (col(t, i, 0) < cols) {
-        load8(row + col(t, i, 0), v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      }
+      unpack4x2(load_raw8(row + at(i, 0)), v);
     } else {
+      float f[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = col(t, i, e) < cols ? to_f32(row[col(t, i, e)]) : 0.f;
+      for (int e = 0; e < 8; ++e) f[e] = at(i, e) < cols ? to_f32(row[at(i, e)]) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = make_float2(f[2 * k], f[2 * k + 1]);
     }
   }
   template <typename T>
-  static __device__ __forceinline__ void store(T* row, int t, int i, int cols, const float (&v)[8]) {
+  static __device__ __forceinline__ void store(T* row, int i, int cols, const float2 (&v)[4]) {
+    const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
     if constexpr (VEC) {
-      if (col(t, i, 0) < cols) store8(row + col(t, i, 0), v);
+      store8(row + at(i, 0), f);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (col(t, i, e) < cols) row[col(t, i, e)] = from_f32<T>(v[e]);
+        if (at(i, e) < cols) row[at(i, e)] = from_f32<T>(f[e]);
+    }
+  }
+  // zeros in the scalar columns past the row (VEC: there are none)
+  static __device__ __forceinline__ void trim(int i, int cols, float2 (&v)[4]) {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (at(i, 2 * k) >= cols) v[k].x = 0.f;
+        if (at(i, 2 * k + 1) >= cols) v[k].y = 0.f;
+      }
     }
   }
 };
 
+// A thread's ring of K stages in shared memory: PER 16-byte pieces per stage, each
+// at its own slot of the block's threads (neighbouring threads, neighbouring
+// slots).
+template <int K, int PER>
+struct Ring {
+  uint4* slots;
+  int threads, tid;
+  __device__ __forceinline__ explicit Ring(void* smem)
+      : slots(static_cast<uint4*>(smem)), threads(blockDim.x * blockDim.y), tid(threadIdx.y * blockDim.x + threadIdx.x) {}
+  __device__ __forceinline__ uint4* slot(int stage, int piece) const {
+    return slots + (stage * PER + piece) * threads + tid;
+  }
+  // 8 elements (sizeof(T) / 2 pieces from `piece` on) of one unit
+  template <typename T>
+  __device__ __forceinline__ void copy(int stage, int piece, const T* src) const {
+#pragma unroll
+    for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) {
+      const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot(stage, piece + h)));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<const uint4*>(src) + h)
+                   : "memory");
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(int stage, int piece, float2 (&v)[4]) const {
+    Raw8<T> r;
+#pragma unroll
+    for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) r.w[h] = *slot(stage, piece + h);
+    unpack4x2(r, v);
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // the oldest of the K stages in flight has arrived
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory"); }
+};
+
+__device__ __forceinline__ void group_barrier() {
+  asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+}
+
+// Sums of N values (a power of two) over a group's threads, the same bits in
+// every thread.  Within a warp the values are halved among the lanes first
+// (lane bit 4 keeps the upper half, and so on), so that N values cost N - 1 +
+// 5 - log2 N exchanges, not 5 N.  `red` holds 2 x N x 32 floats, used
+// alternately, so that one barrier per sum suffices.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) {
+  const int lane = threadIdx.x & 31;
+  int live = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (live > 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= live / 2) break;
+        const float keep = up ? v[i + live / 2] : v[i];
+        const float send = up ? v[i] : v[i + live / 2];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
+      live /= 2;
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  // lane l now has the warp's sum of value l / SPAN
+  constexpr int SPAN = 32 / N;
+  float s = v[0];
+  const int warps = blockDim.x >> 5;
+  if (warps > 1) {
+    const int first = threadIdx.y * warps;
+    float* r = red + flip * N * 32;
+    flip ^= 1;
+    if (lane % SPAN == 0) r[(lane / SPAN) * 32 + first + (threadIdx.x >> 5)] = s;
+    group_barrier();
+    s = 0.f;
+    for (int w = lane % SPAN; w < warps; w += SPAN) s += r[(lane / SPAN) * 32 + first + w];
+#pragma unroll
+    for (int o = SPAN / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * SPAN);
+}
+
 // ---------------------------------------------------------------- forward
-constexpr int kFwdItems = 4;   // 32 columns per thread
-template <typename X, typename Y, int TPR, bool VEC>
-__global__ void __launch_bounds__(TPR < 256 ? (TPR == 32 ? 256 : TPR) : TPR)
-layer_norm_kernel(const NormParams p) {
-  constexpr int ROWS = TPR == 32 ? 8 : 1;   // rows per block
-  using S = Share<TPR, VEC>;
-  __shared__ float red[64];
+// R: rows a group takes at a time; K: stages of R rows in the ring; HOLD: gain
+// and bias stay in registers.
+template <typename X, typename Y, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
+__global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const NormParams p) {
+  using C = Cols<VEC>;
+  constexpr int UP = static_cast<int>(sizeof(X)) / 2;   // 16-byte pieces per unit
+  extern __shared__ uint4 ring_smem[];
+  __shared__ float red[2 * R * 32];
+  const Ring<K, R * UNITS * UP> ring(ring_smem);
+  int flip = 0;
   pdl_launch_dependents();
   pdl_wait();
-  const int t = threadIdx.x % TPR;
-  const long long row = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / TPR;
-  if (row >= p.rows) return;   // ROWS > 1: whole warps
-  int flip = 0;
-  const X* x = static_cast<const X*>(p.x) + row * p.x_ld;
-  float v[kFwdItems][8];
-#pragma unroll
-  for (int i = 0; i < kFwdItems; ++i) S::load(x, t, i, p.cols, v[i]);
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < kFwdItems; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[0] += v[i][e];
-  row_sum<TPR>(s, red, flip);
   const float n = static_cast<float>(p.cols);
-  const float mean = s[0] / n;   // divided, not scaled: the mean of equal values is that value
-  float q[1] = {0.f};
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y * R;
+  long long row0 = (static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y) * R;
+  auto fetch = [&](long long first, int stage) {
+    if constexpr (VEC) {
 #pragma unroll
-  for (int i = 0; i < kFwdItems; ++i)
+      for (int r = 0; r < R; ++r) {
+        if (first + r >= p.rows) break;
+        const X* x = static_cast<const X*>(p.x) + (first + r) * p.x_ld;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[i][e] = S::col(t, i, e) < p.cols ? v[i][e] - mean : 0.f;
-      q[0] = fmaf(v[i][e], v[i][e], q[0]);
+        for (int i = 0; i < UNITS; ++i)
+          if (C::inside(i, p.cols)) ring.copy(stage, (r * UNITS + i) * UP, x + C::at(i, 0));
+      }
     }
-  row_sum<TPR>(q, red, flip);
-  const float rstd = 1.f / sqrtf(q[0] / n + p.eps);
-  if (t == 0) {
-    p.mean[row] = mean;
-    p.rstd[row] = rstd;
+    ring.commit();
+  };
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) fetch(row0 + k * step, k);
+  float2 g[UNITS][4], b[UNITS][4] = {};
+  auto weights = [&](int i) {
+    if (!C::inside(i, p.cols)) return;
+    C::load(p.gain, i, p.cols, g[i]);
+    if (p.bias) C::load(p.bias, i, p.cols, b[i]);
+  };
+  if (HOLD) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) weights(i);
   }
-  Y* y = static_cast<Y*>(p.y) + row * p.y_ld;
+  int stage = 0;
+  for (; row0 < p.rows; row0 += step) {
+    fetch(row0 + (K - 1) * step, stage == 0 ? K - 1 : stage - 1);
+    ring.wait();
+    const int live = static_cast<int>(min(static_cast<long long>(R), p.rows - row0));
+    auto unit = [&](int r, int i, float2 (&v)[4]) {
+      if constexpr (VEC) ring.template get<X>(stage, (r * UNITS + i) * UP, v);
+      else C::load(static_cast<const X*>(p.x) + (row0 + r) * p.x_ld, i, p.cols, v);
+    };
+    float mean[R], rstd[R];
 #pragma unroll
-  for (int i = 0; i < kFwdItems; ++i) {
-    float g[8], b[8] = {};
-    S::load(p.gain, t, i, p.cols, g);
-    if (p.bias) S::load(p.bias, t, i, p.cols, b);
+    for (int r = 0; r < R; ++r) {
+      float2 s = both(0.f);
+      if (r < live)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e] * rstd, g[e], b[e]);
-    S::store(y, t, i, p.cols, v[i]);
+        for (int i = 0; i < UNITS; ++i)
+          if (C::inside(i, p.cols)) {
+            float2 v[4];
+            unit(r, i, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s = __fadd2_rn(s, v[k]);
+          }
+      mean[r] = s.x + s.y;
+    }
+    group_sum<R>(mean, red, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] /= n;   // divided, not scaled: the mean of equal values is that value
+      float2 s = both(0.f);
+      if (r < live)
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+          if (C::inside(i, p.cols)) {
+            float2 v[4];
+            unit(r, i, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __fadd2_rn(v[k], both(-mean[r]));
+            C::trim(i, p.cols, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s = __ffma2_rn(v[k], v[k], s);
+          }
+      rstd[r] = s.x + s.y;
+    }
+    group_sum<R>(rstd, red, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= live) break;
+      rstd[r] = 1.f / sqrtf(rstd[r] / n + p.eps);
+      if (threadIdx.x == 0) {
+        p.mean[row0 + r] = mean[r];
+        p.rstd[row0 + r] = rstd[r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+      if (!C::inside(i, p.cols)) continue;
+      if (!HOLD) weights(i);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r >= live) break;
+        float2 v[4];
+        unit(r, i, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[k], both(-mean[r])), both(rstd[r])), g[i][k], b[i][k]);
+        C::store(static_cast<Y*>(p.y) + (row0 + r) * p.y_ld, i, p.cols, v);
+      }
+    }
+    if (++stage == K) stage = 0;
   }
 }
 
 // --------------------------------------------------------------- backward
-// dgain and dbias sums per thread in shared memory, at slots that only this
-// thread touches: [unit element][thread].
-constexpr int kBwdItems = 2;   // 16 columns per thread
-template <typename X, int TPR, bool VEC>
-__global__ void __launch_bounds__(TPR) layer_norm_grad_kernel(const NormParams p) {
-  using S = Share<TPR, VEC>;
-  __shared__ float red[128];
-  extern __shared__ float acc[];
-  const int t = threadIdx.x;
-  constexpr int E = kBwdItems * 8;
-  float* dg = acc;
-  float* db = acc + E * TPR;
-#pragma unroll
-  for (int e = 0; e < E; ++e) dg[e * TPR + t] = db[e * TPR + t] = 0.f;
+template <typename X, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
+__global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormParams p) {
+  using C = Cols<VEC>;
+  constexpr int UP = static_cast<int>(sizeof(X)) / 2;
+  extern __shared__ uint4 ring_smem[];
+  __shared__ float red[2 * 2 * R * 32];
+  const Ring<K, 2 * R * UNITS * UP> ring(ring_smem);   // per row and unit: x, then dy
   int flip = 0;
+  float2 dg[UNITS][4] = {}, db[UNITS][4] = {}, g[UNITS][4] = {};
   pdl_launch_dependents();
   pdl_wait();
-  const float inv = 1.f / static_cast<float>(p.cols);
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const X* x = static_cast<const X*>(p.x) + row * p.x_ld;
-    const X* dy = static_cast<const X*>(p.dy) + row * p.dy_ld;
-    const float mean = p.mean[row], rstd = p.rstd[row];
-    float xh[kBwdItems][8], gy[kBwdItems][8];
-    float s[2] = {0.f, 0.f};
+  const float n = static_cast<float>(p.cols);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y * R;
+  long long row0 = (static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y) * R;
+  auto fetch = [&](long long first, int stage) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kBwdItems; ++i) {
-      S::load(x, t, i, p.cols, xh[i]);
-      S::load(dy, t, i, p.cols, gy[i]);
-    }
+      for (int r = 0; r < R; ++r) {
+        if (first + r >= p.rows) break;
+        const X* x = static_cast<const X*>(p.x) + (first + r) * p.x_ld;
+        const X* dy = static_cast<const X*>(p.dy) + (first + r) * p.dy_ld;
 #pragma unroll
-    for (int i = 0; i < kBwdItems; ++i) {
-      float g[8];
-      S::load(p.gain, t, i, p.cols, g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xh[i][e] = S::col(t, i, e) < p.cols ? (xh[i][e] - mean) * rstd : 0.f;
-        float* a = dg + (i * 8 + e) * TPR + t;
-        float* b = db + (i * 8 + e) * TPR + t;
-        *a = fmaf(gy[i][e], xh[i][e], *a);
-        *b += gy[i][e];
-        gy[i][e] *= g[e];
-        s[0] += gy[i][e];
-        s[1] = fmaf(gy[i][e], xh[i][e], s[1]);
+        for (int i = 0; i < UNITS; ++i)
+          if (C::inside(i, p.cols)) {
+            ring.copy(stage, (r * UNITS + i) * 2 * UP, x + C::at(i, 0));
+            ring.copy(stage, (r * UNITS + i) * 2 * UP + UP, dy + C::at(i, 0));
+          }
       }
     }
-    row_sum<TPR>(s, red, flip);
-    const float c1 = s[0] * inv, c2 = s[1] * inv;
-    X* dx = static_cast<X*>(p.y) + row * p.y_ld;
+    ring.commit();
+  };
+  float mean_next[R], rstd_next[R];
+  auto stats = [&](long long first) {
 #pragma unroll
-    for (int i = 0; i < kBwdItems; ++i) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) gy[i][e] = rstd * (gy[i][e] - c1 - xh[i][e] * c2);
-      S::store(dx, t, i, p.cols, gy[i]);
+    for (int r = 0; r < R; ++r) {
+      mean_next[r] = first + r < p.rows ? p.mean[first + r] : 0.f;
+      rstd_next[r] = first + r < p.rows ? p.rstd[first + r] : 0.f;
     }
+  };
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) fetch(row0 + k * step, k);
+  stats(row0);
+  if (HOLD) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i)
+      if (C::inside(i, p.cols)) C::load(p.gain, i, p.cols, g[i]);
   }
-  float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+  int stage = 0;
+  for (; row0 < p.rows; row0 += step) {
+    float mean[R], rstd[R];
 #pragma unroll
-  for (int i = 0; i < kBwdItems; ++i)
+    for (int r = 0; r < R; ++r) {
+      mean[r] = mean_next[r];
+      rstd[r] = rstd_next[r];
+    }
+    fetch(row0 + (K - 1) * step, stage == 0 ? K - 1 : stage - 1);
+    stats(row0 + step);
+    ring.wait();
+    const int live = static_cast<int>(min(static_cast<long long>(R), p.rows - row0));
+    // xh and dy of a unit that is inside, zeros past the row
+    auto unit = [&](int r, int i, float2 (&xh)[4], float2 (&dy)[4]) {
+      if constexpr (VEC) {
+        ring.template get<X>(stage, (r * UNITS + i) * 2 * UP, xh);
+        ring.template get<X>(stage, (r * UNITS + i) * 2 * UP + UP, dy);
+      } else {
+        C::load(static_cast<const X*>(p.x) + (row0 + r) * p.x_ld, i, p.cols, xh);
+        C::load(static_cast<const X*>(p.dy) + (row0 + r) * p.dy_ld, i, p.cols, dy);
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = S::col(t, i, e);
-      if (c < p.cols) {
-        out[c] = dg[(i * 8 + e) * TPR + t];
-        out[p.cols + c] = db[(i * 8 + e) * TPR + t];
+      for (int k = 0; k < 4; ++k) xh[k] = __fmul2_rn(__fadd2_rn(xh[k], both(-mean[r])), both(rstd[r]));
+      C::trim(i, p.cols, xh);
+    };
+    float s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 s1 = both(0.f), s2 = both(0.f);
+      if (r < live)
+#pragma unroll
+        for (int i = 0; i < UNITS; ++i)
+          if (C::inside(i, p.cols)) {
+            float2 xh[4], dy[4];
+            unit(r, i, xh, dy);
+            if (!HOLD) C::load(p.gain, i, p.cols, g[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              dg[i][k] = __ffma2_rn(dy[k], xh[k], dg[i][k]);
+              db[i][k] = __fadd2_rn(db[i][k], dy[k]);
+              const float2 gy = __fmul2_rn(dy[k], g[i][k]);
+              s1 = __fadd2_rn(s1, gy);
+              s2 = __ffma2_rn(gy, xh[k], s2);
+            }
+          }
+      s[2 * r] = s1.x + s1.y;
+      s[2 * r + 1] = s2.x + s2.y;
+    }
+    group_sum<2 * R>(s, red, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= live) break;
+      const float2 c1 = both(-s[2 * r] / n), c2 = both(-s[2 * r + 1] / n);
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i) {
+        if (!C::inside(i, p.cols)) continue;
+        float2 xh[4], dy[4];
+        unit(r, i, xh, dy);
+        if (!HOLD) C::load(p.gain, i, p.cols, g[i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dy[k] = __fmul2_rn(__ffma2_rn(xh[k], c2, __ffma2_rn(dy[k], g[i][k], c1)), both(rstd[r]));
+        C::store(static_cast<X*>(p.y) + (row0 + r) * p.y_ld, i, p.cols, dy);
       }
     }
+    if (++stage == K) stage = 0;
+  }
+  if (blockDim.y > 1) __syncthreads();   // the ring is done with
+  float* fold = reinterpret_cast<float*>(ring_smem);
+  // the groups' sums, in order
+  for (int k = 0; k < static_cast<int>(blockDim.y); ++k) {
+    if (static_cast<int>(threadIdx.y) == k) {
+      float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+      const bool last = k == static_cast<int>(blockDim.y) - 1;
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = C::at(i, e);
+          if (c >= p.cols) continue;
+          float vg = e & 1 ? dg[i][e >> 1].y : dg[i][e >> 1].x, vb = e & 1 ? db[i][e >> 1].y : db[i][e >> 1].x;
+          if (k > 0) {
+            vg += fold[c];
+            vb += fold[p.cols + c];
+          }
+          (last ? out : fold)[c] = vg;
+          (last ? out : fold)[p.cols + c] = vb;
+        }
+    }
+    if (blockDim.y > 1) __syncthreads();
+  }
 }
 
 // dgain / dbias (+)= the blocks' partial rows, added in a fixed tree: 16
@@ -223,7 +433,7 @@ __global__ void __launch_bounds__(32 * kColThreads) layer_norm_column_kernel(con
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < p.cols)
-#pragma unroll 4
+#pragma unroll 8
     for (int b = w; b < p.blocks; b += kColThreads)
       s += p.partial[(static_cast<long long>(b) * 2 + which) * p.cols + c];
   part[w][lane] = s;
@@ -238,65 +448,105 @@ __global__ void __launch_bounds__(32 * kColThreads) layer_norm_column_kernel(con
 }
 
 // ---------------------------------------------------------------- launchers
-template <typename X, typename Y, int TPR, bool VEC>
+namespace {
+int round32(int x) { return (x + 31) / 32 * 32; }
+// Threads and groups of a block for rows of `units` 8-column units.
+dim3 norm_block(int units_per_thread, int cols) {
+  const int units = (cols + 7) / 8;
+  const int t = round32((units + units_per_thread - 1) / units_per_thread);
+  const int g = t >= kNormThreads ? 1 : kNormThreads / t;
+  return dim3(t, g > 15 ? (t == 32 ? 16 : 15) : g);
+}
+}  // namespace
+
+template <typename X, typename Y, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
 static cudaError_t forward_launch(const NormParams& p, cudaStream_t s) {
-  constexpr int ROWS = TPR == 32 ? 8 : 1;
-  return launch_pdl(layer_norm_kernel<X, Y, TPR, VEC>, dim3(static_cast<unsigned>((p.rows + ROWS - 1) / ROWS)),
-                    dim3(TPR * ROWS), 0, s, p);
+  dim3 block = norm_block(UNITS, p.cols);
+  // a block of several groups only where there are rows for every SM
+  while (block.y > 1 && static_cast<long long>(block.y) * R * p.sms > p.rows) block.y = (block.y + 1) / 2;
+  auto kern = layer_norm_kernel<X, Y, VEC, UNITS, MAXT, MINB, R, K, HOLD>;
+  const size_t smem = VEC ? static_cast<size_t>(K) * R * UNITS * 8 * sizeof(X) * block.x * block.y : 0;
+  if (smem > 32 * 1024) {   // beyond the default limit of 48 KB with the static part
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const long long per = static_cast<long long>(block.y) * R;
+  const long long want = (p.rows + per - 1) / per, cap = static_cast<long long>(p.sms) * MINB * (MAXT / (block.x * block.y));
+  return launch_pdl(kern, dim3(static_cast<unsigned>(want < cap ? want : cap)), block, smem, s, p);
 }
 template <typename X, typename Y, bool VEC>
-static cudaError_t forward_width(const NormParams& p, cudaStream_t s) {
-  constexpr int E = kFwdItems * 8;
-  if (p.cols <= 32 * E) return forward_launch<X, Y, 32, VEC>(p, s);
-  if (p.cols <= 64 * E) return forward_launch<X, Y, 64, VEC>(p, s);
-  if (p.cols <= 128 * E) return forward_launch<X, Y, 128, VEC>(p, s);
-  if (p.cols <= 256 * E) return forward_launch<X, Y, 256, VEC>(p, s);
-  return forward_launch<X, Y, 512, VEC>(p, s);
+static cudaError_t forward_shape(const NormParams& p, cudaStream_t s) {
+  // one row at a time while every group gets a few at most
+  const bool few = p.rows <= 8ll * p.sms;
+  constexpr bool B16 = sizeof(X) == 2;
+  if (p.cols <= 2048)
+    return few ? forward_launch<X, Y, VEC, 1, kNormThreads, 4, 1, 2, true>(p, s)
+               : forward_launch<X, Y, VEC, 1, kNormThreads, 4, 4, 2, true>(p, s);
+  if (p.cols <= 4096)
+    return few ? forward_launch<X, Y, VEC, 2, kNormThreads, 3, 1, 2, true>(p, s)
+               : forward_launch<X, Y, VEC, 2, kNormThreads, 3, B16 ? 4 : 2, 2, true>(p, s);
+  if (p.cols <= 8192) return forward_launch<X, Y, VEC, 2, 512, 1, B16 ? 4 : 2, 2, true>(p, s);
+  return forward_launch<X, Y, VEC, 2, 1024, 1, B16 ? 2 : 1, 2, false>(p, s);
 }
 template <typename X, typename Y>
 static cudaError_t forward_typed(const NormParams& p, cudaStream_t s) {
-  return p.vec ? forward_width<X, Y, true>(p, s) : forward_width<X, Y, false>(p, s);
+  return p.vec ? forward_shape<X, Y, true>(p, s) : forward_shape<X, Y, false>(p, s);
 }
-static_assert(512 * kFwdItems * 8 >= kNormMaxCols && 1024 * kBwdItems * 8 >= kNormMaxCols, "row capacity");
+static_assert(1024 * 2 * 8 >= kNormMaxCols, "row capacity");
 cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s) {
   using B = __nv_bfloat16;
   if (p.x_bf16) return p.y_bf16 ? forward_typed<B, B>(p, s) : forward_typed<B, float>(p, s);
   return p.y_bf16 ? forward_typed<float, B>(p, s) : forward_typed<float, float>(p, s);
 }
 
-static int grad_threads(int cols) {
-  for (int t = 32; t < 1024; t *= 2)
-    if (cols <= t * kBwdItems * 8) return t;
-  return 1024;
+// The backward kernel's classes of widths: units per thread, largest block, blocks per SM.
+struct GradClass {
+  int units, max_threads, per_sm;
+};
+static GradClass grad_class(int cols) {
+  if (cols <= 2048) return {1, kNormThreads, 3};
+  if (cols <= 4096) return {2, kNormThreads, 2};
+  if (cols <= 8192) return {2, 512, 1};
+  return {2, 1024, 1};
 }
 int layer_norm_grad_blocks(long long rows, int cols, int sms) {
-  const int per_sm = 1024 / grad_threads(cols);   // blocks an SM holds: 1024 threads
-  const long long cap = static_cast<long long>(sms) * (per_sm > 8 ? 8 : per_sm);
-  return static_cast<int>(rows < cap ? rows : cap);
+  const GradClass c = grad_class(cols);
+  const dim3 block = norm_block(c.units, cols);
+  const long long per_sm = static_cast<long long>(c.per_sm) * (c.max_threads / (block.x * block.y));
+  // few rows: two blocks per SM at most, so that few partial rows are left to add
+  const long long want = (rows + block.y - 1) / block.y;
+  const long long cap = sms * (want < 8 * sms && per_sm > 2 ? 2 : per_sm);
+  return static_cast<int>(want < cap ? want : cap);
 }
-template <typename X, int TPR, bool VEC>
+template <typename X, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
 static cudaError_t backward_launch(const NormParams& p, cudaStream_t s) {
-  constexpr int kSmem = 2 * kBwdItems * 8 * TPR * 4;
-  const cudaError_t e = cudaFuncSetAttribute(layer_norm_grad_kernel<X, TPR, VEC>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(layer_norm_grad_kernel<X, TPR, VEC>, dim3(p.blocks), dim3(TPR), kSmem, s, p);
+  const dim3 block = norm_block(UNITS, p.cols);
+  auto kern = layer_norm_grad_kernel<X, VEC, UNITS, MAXT, MINB, R, K, HOLD>;
+  size_t smem = VEC ? static_cast<size_t>(K) * R * 2 * UNITS * 8 * sizeof(X) * block.x * block.y : 0;
+  if (block.y > 1) smem = smem > static_cast<size_t>(8) * p.cols ? smem : static_cast<size_t>(8) * p.cols;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(p.blocks), block, smem, s, p);
 }
 template <typename X, bool VEC>
-static cudaError_t backward_width(const NormParams& p, cudaStream_t s) {
-  switch (grad_threads(p.cols)) {
-    case 32: return backward_launch<X, 32, VEC>(p, s);
-    case 64: return backward_launch<X, 64, VEC>(p, s);
-    case 128: return backward_launch<X, 128, VEC>(p, s);
-    case 256: return backward_launch<X, 256, VEC>(p, s);
-    case 512: return backward_launch<X, 512, VEC>(p, s);
-    default: return backward_launch<X, 1024, VEC>(p, s);
-  }
+static cudaError_t backward_shape(const NormParams& p, cudaStream_t s) {
+  constexpr bool B16 = sizeof(X) == 2;
+  const bool few = p.rows <= 8ll * p.sms;   // one row at a time
+  if (p.cols <= 2048)
+    return few ? backward_launch<X, VEC, 1, kNormThreads, 3, 1, 4, true>(p, s)
+               : backward_launch<X, VEC, 1, kNormThreads, 3, 2, 2, true>(p, s);
+  if (p.cols <= 4096) return backward_launch<X, VEC, 2, kNormThreads, 2, B16 ? 2 : 1, 2, true>(p, s);
+  if (p.cols <= 8192) return backward_launch<X, VEC, 2, 512, 1, B16 ? 2 : 1, 2, true>(p, s);
+  return backward_launch<X, VEC, 2, 1024, 1, 1, B16 ? 3 : 1, false>(p, s);
+}
+template <typename X>
+static cudaError_t backward_typed(const NormParams& p, cudaStream_t s) {
+  return p.vec ? backward_shape<X, true>(p, s) : backward_shape<X, false>(p, s);
 }
 cudaError_t launch_layer_norm_grad(const NormParams& p, cudaStream_t s) {
-  using B = __nv_bfloat16;
-  if (p.x_bf16) return p.vec ? backward_width<B, true>(p, s) : backward_width<B, false>(p, s);
-  return p.vec ? backward_width<float, true>(p, s) : backward_width<float, false>(p, s);
+  return p.x_bf16 ? backward_typed<__nv_bfloat16>(p, s) : backward_typed<float>(p, s);
 }
 cudaError_t launch_layer_norm_columns(const NormParams& p, cudaStream_t s) {
   const dim3 grid((p.cols + 31) / 32, p.dbias ? 2 : 1);
