@@ -364,8 +364,8 @@ muon_status muon_embedding_forward(const void* table, int32_t table_dtype, int64
  * grad[v] <- (grad[v] +) scale * sum over t with ids[t] = v of dout[t], for
  * every row v of the table; ids outside [0, vocab) contribute nothing.  The
  * ids are sorted on the device (stable), and each row of grad is summed by
- * ascending t in one place; runs of more than 128 equal ids are summed in
- * chunks of 32 first.  With `accumulate`, rows whose id does not occur are
+ * ascending t in one place; runs of more than 32 equal ids are summed in
+ * parts that depend on the run's length alone.  With `accumulate`, rows whose id does not occur are
  * neither read nor written.
  */
 size_t muon_embedding_grad_workspace_size(int64_t vocab, int64_t dim, int64_t n);

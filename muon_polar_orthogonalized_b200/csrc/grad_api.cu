@@ -83,15 +83,17 @@ muon_status check_embedding(int64_t vocab, int64_t dim, int64_t n, int32_t ids_b
 }
 
 struct EmbedWs {
-  size_t keys, pos, runs, partial, total;
+  size_t keys, runs, items, joins, partial, total;
 };
 EmbedWs embed_ws(int64_t vocab, int64_t dim, int64_t n) {
   EmbedWs w;
   w.keys = up256(static_cast<size_t>(n) * 4);
-  w.pos = w.keys;
   w.runs = up256(static_cast<size_t>(vocab) * 4);
-  w.partial = up256(static_cast<size_t>(n / kEmbedChunk) * dim * 4);
-  w.total = 256 + 2 * w.keys + 2 * w.pos + 2 * w.runs + w.partial;
+  w.items = up256(static_cast<size_t>(embed_max_items(n)) * 16);
+  w.joins = up256(static_cast<size_t>(n / (kEmbedPiece + 1)) * 16);
+  // a run of several pieces has less than two slots per kEmbedPiece positions
+  w.partial = up256(static_cast<size_t>(n / kEmbedPiece + n / (kEmbedPiece + 1)) * dim * 4);
+  w.total = 256 + 5 * w.keys + 2 * w.runs + w.items + w.joins + w.partial;
   return w;
 }
 
@@ -250,22 +252,27 @@ muon_status muon_embedding_grad(const void* dout, int32_t dout_dtype, int64_t do
       return r;
     };
     for (int i = 0; i < 2; ++i) p.keys[i] = reinterpret_cast<uint32_t*>(take(w.keys));
-    for (int i = 0; i < 2; ++i) p.pos[i] = reinterpret_cast<uint32_t*>(take(w.pos));
+    for (int i = 0; i < 2; ++i) p.pos[i] = reinterpret_cast<uint32_t*>(take(w.keys));
+    p.offset = reinterpret_cast<uint32_t*>(take(w.keys));
     p.lo = reinterpret_cast<uint32_t*>(take(w.runs));
     p.hi = reinterpret_cast<uint32_t*>(take(w.runs));
+    p.counts = reinterpret_cast<EmbedCounts*>(p.status + 4);
+    p.items = reinterpret_cast<uint4*>(take(w.items));
+    p.joins = reinterpret_cast<uint4*>(take(w.joins));
     p.partial = reinterpret_cast<float*>(take(w.partial));
-    // keys 0 .. vocab (vocab: no token), in as few passes of at most 9 bits as they need
+    p.sms = sms;
+    // keys 0 .. vocab (vocab: no token), in passes of 9 bits
     int width = 1;
     while ((vocab >> width) != 0) ++width;
     p.passes = (width + 8) / 9;
-    p.bits = (width + p.passes - 1) / p.passes;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     st = launched(api_timed_launch(K_EMBED_SORT, s, [&] { return launch_embedding_sort(p, s); }),
                   "embedding sort launch");
     if (st != MUON_OK) return st;
-    if (n > kEmbedLongRun) {   // else no run is long
-      st = launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_chunks(p, s); }),
-                    "embedding chunk launch");
+    for (int join = 0; join < 2; ++join) {
+      if (n <= (join ? kEmbedPiece : kEmbedLongRun)) break;   // no run is that long
+      st = launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_long(p, join != 0, s); }),
+                    "embedding long-run launch");
       if (st != MUON_OK) return st;
     }
     return launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_rows(p, s); }),

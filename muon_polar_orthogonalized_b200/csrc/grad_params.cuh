@@ -20,8 +20,14 @@ struct EmbedParams {
   float scale;
 };
 
-constexpr int kEmbedChunk = 32;        // sorted positions per chunk of a long run
-constexpr int kEmbedLongRun = 128;     // runs of one token longer than this are summed by chunks
+constexpr int kEmbedLongRun = 32;      // runs of one token longer than this are cut into
+constexpr int kEmbedPiece = 128;       // pieces of this many sorted positions
+constexpr uint32_t kEmbedNoSlot = 0xffffffffu;
+// Most pieces that n positions can make.
+inline long long embed_max_items(long long n) { return n / kEmbedPiece + n / (kEmbedLongRun + 1); }
+struct EmbedCounts {
+  uint32_t items, slots, joins;
+};
 
 struct EmbedGradParams {
   const void* dout;    // [n, dim], row pitch dout_ld elements
@@ -38,8 +44,13 @@ struct EmbedGradParams {
   uint32_t* pos[2];    // ... and the positions they come from
   uint32_t* lo;        // [vocab] first and one past the last sorted position of each id
   uint32_t* hi;
-  float* partial;      // [n / kEmbedChunk][dim] sums of whole chunks of long runs
-  int passes, bits;    // radix sort: passes of `bits` bits
+  uint32_t* offset;    // [n] a key's offset within its warp and digit
+  EmbedCounts* counts;
+  uint4* items;        // pieces: (id, first and one past the last sorted position, slot or kEmbedNoSlot)
+  uint4* joins;        // runs of several pieces: (id, first and one past the last slot, -)
+  float* partial;      // [slot][dim] sums of the pieces of such runs
+  int passes;          // of the radix sort, 9 bits each
+  int sms;
 };
 
 // ------------------------------------------------------------ layer norm
@@ -102,7 +113,7 @@ struct alignas(64) WeightGradTc {
 
 cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s);
 cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s);
-cudaError_t launch_embedding_chunks(const EmbedGradParams& p, cudaStream_t s);
+cudaError_t launch_embedding_long(const EmbedGradParams& p, bool join, cudaStream_t s);
 cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s);
 cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s);
 cudaError_t launch_layer_norm_grad(const NormParams& p, cudaStream_t s);

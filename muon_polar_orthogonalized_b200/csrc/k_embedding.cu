@@ -11,9 +11,8 @@
 // row and column segment sums the run in order and writes the row once (an
 // empty run writes zeros, or nothing when accumulating).  Frequent tokens
 // have runs of thousands of positions; runs longer than kEmbedLongRun are cut
-// at multiples of kEmbedChunk sorted positions, every whole chunk is summed
-// by its own warp into the workspace, and the row's warp adds the ragged
-// head, the chunk sums and the ragged tail, again in order.
+// into pieces of kEmbedPiece positions, a block sums each piece (eight warps, an
+// eighth each), and the pieces of a run are added in order by another block.
 //
 // The sort is a least-significant-digit radix sort (stable, so positions stay
 // ascending within an id) by ONE thread-block cluster: the blocks exchange
@@ -24,6 +23,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "grad_params.cuh"
 #include "pdl.cuh"
 #include "vec8.cuh"
@@ -31,8 +33,23 @@
 namespace muon {
 namespace cg = cooperative_groups;
 
-constexpr int kEmbThreads = 256;
-constexpr int kEmbWarps = kEmbThreads / 32;
+// Launch shape of the streaming kernels: blocks of eight warps, `wx` side by
+// side along a row and 8 / wx rows apart, over a grid of (rows, row pieces);
+// a warp takes a piece of a row, and where rows are short, its lanes share
+// them out in groups of `lpr` lanes, a row each.  No index is divided.
+constexpr int kEmbWarps = 8;
+constexpr int kSegUnits = 4;    // 8-column units per lane: lookup
+constexpr int kSumUnits = 2;    // and gradient, which holds sums and several rows' units in registers
+struct EmbedShape {
+  int lpr;        // lanes per row: 32, or fewer for rows of at most lpr * 8 * units columns
+  int wx;
+  int cols;       // of a warp: 32 * 8 * units
+};
+// Lane `l` of `lpr` holds, in unit u, 8 adjacent columns (VEC) or 8 that lie lpr apart.
+template <bool VEC>
+__device__ __forceinline__ int seg_col(int c0, int lpr, int l, int u, int e) {
+  return VEC ? c0 + (u * lpr + l) * 8 + e : c0 + (u * 8 + e) * lpr + l;
+}
 
 // The row of the table a token asks for, or -1.
 __device__ __forceinline__ long long token_row(const void* ids, int ids64, long long t, long long vocab) {
@@ -40,39 +57,58 @@ __device__ __forceinline__ long long token_row(const void* ids, int ids64, long 
   return (id >= 0 && id < vocab) ? id : -1;
 }
 
-// Columns per warp task: 8 per lane and unit with 16-byte accesses, or single
-// columns, lanes adjacent.
-template <bool VEC>
-constexpr int kSegCols = VEC ? 256 : 128;
+// This lane's row (of the grid's rows) and its first column.
+struct LaneRow {
+  long long row;
+  int l, c0;
+};
+__device__ __forceinline__ LaneRow lane_row(const EmbedShape& sh) {
+  const int lane = threadIdx.x, per_warp = 32 / sh.lpr;
+  const long long slot = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
+  return {slot * per_warp + lane / sh.lpr, lane % sh.lpr, static_cast<int>(blockIdx.y * sh.wx + threadIdx.y) * sh.cols};
+}
 
-// One warp per (token, column segment).
 template <typename T, typename O, bool VEC>
-__global__ void __launch_bounds__(kEmbThreads) embedding_kernel(const EmbedParams p, int nseg) {
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_kernel(const EmbedParams p, const EmbedShape sh) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long task = static_cast<long long>(blockIdx.x) * kEmbWarps + (threadIdx.x >> 5);
-  const long long t = task / nseg;
-  if (t >= p.n) return;
-  const int lane = threadIdx.x & 31;
-  const int c0 = static_cast<int>(task - t * nseg) * kSegCols<VEC>;
-  const long long row = token_row(p.ids, p.ids64, t, p.vocab);
+  const LaneRow w = lane_row(sh);
+  if (w.row >= p.n || w.c0 >= p.dim) return;
+  const long long row = token_row(p.ids, p.ids64, w.row, p.vocab);
   const T* src = static_cast<const T*>(p.table) + (row < 0 ? 0 : row) * p.dim;
-  O* dst = static_cast<O*>(p.out) + t * p.out_ld;
+  O* dst = static_cast<O*>(p.out) + w.row * p.out_ld;
   if constexpr (VEC) {
-    const int c = c0 + lane * 8;
-    if (c >= p.dim) return;
-    float v[8] = {};
-    if (row >= 0) {
-      load8(src + c, v);
+    Raw8<T> r[kSegUnits];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= p.scale;
+    for (int u = 0; u < kSegUnits; ++u) {
+      const int c = seg_col<true>(w.c0, sh.lpr, w.l, u, 0);
+      r[u] = Raw8<T>{};
+      if (row >= 0 && c < p.dim) r[u] = load_raw8(src + c);
     }
-    store8(dst + c, v);
+#pragma unroll
+    for (int u = 0; u < kSegUnits; ++u) {
+      const int c = seg_col<true>(w.c0, sh.lpr, w.l, u, 0);
+      if (c >= p.dim) break;
+      float v[8];
+      unpack8(r[u], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = row < 0 ? 0.f : v[e] * p.scale;
+      store8(dst + c, v);
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k * 32 + lane;
-      if (c < p.dim) dst[c] = from_f32<O>(row < 0 ? 0.f : to_f32(src[c]) * p.scale);
+    for (int u = 0; u < kSegUnits; ++u) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = seg_col<false>(w.c0, sh.lpr, w.l, u, e);
+        v[e] = row >= 0 && c < p.dim ? to_f32(src[c]) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = seg_col<false>(w.c0, sh.lpr, w.l, u, e);
+        if (c < p.dim) dst[c] = from_f32<O>(row < 0 ? 0.f : v[e] * p.scale);
+      }
     }
   }
 }
@@ -80,84 +116,128 @@ __global__ void __launch_bounds__(kEmbThreads) embedding_kernel(const EmbedParam
 // ------------------------------------------------------------------- sort
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortMaxBits = 9;
-constexpr int kSortBins = 1 << kSortMaxBits;
-constexpr int kSortCluster = 8;
-constexpr int kSortSmem = (kSortWarps * kSortBins + 2 * kSortBins) * 4;
+constexpr int kSortBits = 9;
+constexpr int kSortBins = 1 << kSortBits;
+constexpr int kSortKeys = 8;         // keys a lane has in flight
+constexpr int kSortSmem = (kSortWarps + 2) * kSortBins * 4;
 
-// Lanes of the warp that hold the same digit as this one.
-__device__ __forceinline__ uint32_t same_digit(uint32_t active, uint32_t d) { return __match_any_sync(active, d); }
+// Lanes of `act` with the same digit: one ballot per bit.  (The match
+// instruction, and a loop over a run-time number of bits, each took 2 to 3
+// times as long.)
+__device__ __forceinline__ uint32_t same_digit(uint32_t act, uint32_t d) {
+  uint32_t peers = act;
+#pragma unroll
+  for (int b = 0; b < kSortBits; ++b) {
+    const bool set = d & (1u << b);
+    const uint32_t m = __ballot_sync(act, set);
+    peers &= set ? m : ~m;
+  }
+  return peers;
+}
 
+// Each warp owns one contiguous range of positions.  Counting, it takes its
+// keys 32 at a time, in order: lanes with the same digit find one another, a
+// key's offset is the warp's count of the digit so far plus the earlier lanes
+// of the 32, and the first of them adds their number to the count in shared
+// memory.  Placing, a key goes to the start of its digit, plus what earlier
+// blocks and warps hold of it, plus its offset.
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const EmbedGradParams p) {
   extern __shared__ uint32_t sm[];
   uint32_t* hist = sm;                                  // [warp][bin]
   uint32_t* total = sm + kSortWarps * kSortBins;        // [bin] of this block, read by the cluster
-  uint32_t* scan = total + kSortBins;                   // [bin]
+  uint32_t* start = total + kSortBins;                  // [bin] of this block's first key
   __shared__ uint32_t warp_sum[kSortWarps];
   cg::cluster_group cluster = cg::this_cluster();
-  const int nb = static_cast<int>(cluster.num_blocks());
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bins = 1 << p.bits;
+  const uint32_t nb = cluster.num_blocks(), rank = cluster.block_rank();
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t n = static_cast<uint32_t>(p.n), vocab = static_cast<uint32_t>(p.vocab);
   pdl_launch_dependents();
   pdl_wait();
 
-  if (rank == 0 && tid == 0) *p.status = 0;
-  // no id has been seen yet
-  for (long long v = static_cast<long long>(rank) * kSortThreads + tid; v < p.vocab;
-       v += static_cast<long long>(nb) * kSortThreads) {
-    p.lo[v] = 0;
-    p.hi[v] = 0;
+  if (rank == 0 && tid == 0) {
+    *p.status = 0;
+    p.counts->items = p.counts->slots = p.counts->joins = 0;
   }
-  // each warp owns one contiguous range of positions, a multiple of 32 long
-  const long long warps = static_cast<long long>(nb) * kSortWarps;
-  const long long per = ((p.n + warps - 1) / warps + 31) / 32 * 32;
-  const long long begin = (static_cast<long long>(rank) * kSortWarps + warp) * per;
-  const long long end = begin + per < p.n ? begin + per : p.n;
+  // no id has been seen yet (the arrays are padded to whole 16-byte units)
+  for (uint32_t v = rank * kSortThreads + tid; v < (vocab + 3) / 4; v += nb * kSortThreads) {
+    reinterpret_cast<uint4*>(p.lo)[v] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(p.hi)[v] = make_uint4(0, 0, 0, 0);
+  }
+  const uint32_t warps = nb * kSortWarps;
+  const uint32_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const uint32_t begin = min(n, (rank * kSortWarps + warp) * per), end = min(n, begin + per);
 
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * p.bits;
+    const int shift = pass * kSortBits;
     const uint32_t* kin = p.keys[(pass + 1) & 1];
     const uint32_t* pin = p.pos[(pass + 1) & 1];
     uint32_t* kout = p.keys[pass & 1];
     uint32_t* pout = p.pos[pass & 1];
-    auto key_at = [&](long long i) -> uint32_t {
-      if (pass) return kin[i];
-      const long long row = token_row(p.ids, p.ids64, i, p.vocab);
-      return static_cast<uint32_t>(row < 0 ? p.vocab : row);
-    };
-    for (int b = tid; b < kSortWarps * bins; b += kSortThreads) hist[(b / bins) * kSortBins + (b % bins)] = 0;
-    __syncthreads();
-    uint32_t* mine = hist + warp * kSortBins;
-    for (long long i0 = begin; i0 < end; i0 += 32) {
-      const long long i = i0 + lane;
-      const uint32_t act = __ballot_sync(0xffffffffu, i < end);
-      if (i < end) {
-        const uint32_t d = (key_at(i) >> shift) & (bins - 1);
-        const uint32_t peers = same_digit(act, d);
-        if (lane == __ffs(peers) - 1) mine[d] += __popc(peers);
+    // kSortKeys keys of this lane from position i0 on, 32 positions apart
+    auto load_keys = [&](uint32_t i0, uint32_t (&key)[kSortKeys]) {
+#pragma unroll
+      for (int k = 0; k < kSortKeys; ++k) {
+        const uint32_t i = i0 + k * 32 + lane;
+        key[k] = 0;
+        if (i < end) {
+          if (pass) {
+            key[k] = kin[i];
+          } else {
+            const long long row = token_row(p.ids, p.ids64, i, p.vocab);
+            key[k] = row < 0 ? vocab : static_cast<uint32_t>(row);
+          }
+        }
       }
-      __syncwarp();
+    };
+    uint32_t* mine = hist + warp * kSortBins;
+#pragma unroll
+    for (int b = 0; b < kSortBins; b += 128) *reinterpret_cast<uint4*>(mine + b + lane * 4) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortKeys) {
+      uint32_t key[kSortKeys];
+      load_keys(i0, key);
+#pragma unroll
+      for (int k = 0; k < kSortKeys; ++k) {
+        if (i0 + k * 32 >= end) break;
+        const uint32_t i = i0 + k * 32 + lane;
+        const uint32_t act = __ballot_sync(0xffffffffu, i < end);
+        if (i < end) {
+          const uint32_t d = (key[k] >> shift) & (kSortBins - 1);
+          const uint32_t peers = same_digit(act, d);
+          const uint32_t rk = __popc(peers & ((1u << lane) - 1)), so_far = mine[d];
+          p.offset[i] = so_far + rk;
+          __syncwarp(act);
+          if (rk == 0) mine[d] = so_far + __popc(peers);
+        }
+        __syncwarp();
+      }
     }
     __syncthreads();
     // per bin: exclusive scan over this block's warps
-    if (tid < bins) {
-      uint32_t run = 0;
+    uint32_t own = 0;
+    if (tid < kSortBins) {
+      uint32_t c[kSortWarps];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * kSortBins + tid];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = hist[w * kSortBins + tid];
-        hist[w * kSortBins + tid] = run;
-        run += c;
+        hist[w * kSortBins + tid] = own;
+        own += c[w];
       }
-      total[tid] = run;
+      total[tid] = own;
     }
-    cluster.sync();
     // per bin: counts of the blocks before this one, and of all blocks
-    uint32_t before = 0, all = 0;
-    if (tid < bins) {
-      for (int r = 0; r < nb; ++r) {
-        const uint32_t c = cluster.map_shared_rank(total, r)[tid];
-        if (r < rank) before += c;
-        all += c;
+    uint32_t before = 0, all = own;
+    if (nb > 1) {
+      cluster.sync();
+      if (tid < kSortBins) {
+        all = 0;
+#pragma unroll 4
+        for (uint32_t r = 0; r < nb; ++r) {
+          const uint32_t c = cluster.map_shared_rank(total, r)[tid];
+          if (r < rank) before += c;
+          all += c;
+        }
       }
     }
     // exclusive scan of `all` over the bins
@@ -169,175 +249,258 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-      uint32_t s = warp_sum[lane];
+    if (tid < kSortBins) {
+      uint32_t left = 0;
+      for (uint32_t w = 0; w < warp; ++w) left += warp_sum[w];
+      start[tid] = inc - all + left + before;
+    }
+    __syncthreads();
+    for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortKeys) {
+      uint32_t key[kSortKeys], from[kSortKeys], off[kSortKeys];
+      load_keys(i0, key);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
+      for (int k = 0; k < kSortKeys; ++k) {
+        const uint32_t i = i0 + k * 32 + lane;
+        from[k] = pass && i < end ? pin[i] : i;
+        off[k] = i < end ? p.offset[i] : 0;
       }
-      warp_sum[lane] = s;
-    }
-    __syncthreads();
-    if (tid < bins) scan[tid] = inc - all + (warp ? warp_sum[warp - 1] : 0) + before;
-    __syncthreads();
-    for (long long i0 = begin; i0 < end; i0 += 32) {
-      const long long i = i0 + lane;
-      const uint32_t act = __ballot_sync(0xffffffffu, i < end);
-      if (i < end) {
-        const uint32_t key = key_at(i);
-        const uint32_t from = pass ? pin[i] : static_cast<uint32_t>(i);
-        const uint32_t d = (key >> shift) & (bins - 1);
-        const uint32_t peers = same_digit(act, d);
-        const uint32_t rk = __popc(peers & ((1u << lane) - 1));
-        const uint32_t dst = scan[d] + mine[d] + rk;
-        __syncwarp(act);
-        if (rk == 0) mine[d] += __popc(peers);
-        kout[dst] = key;
-        pout[dst] = from;
+#pragma unroll
+      for (int k = 0; k < kSortKeys; ++k) {
+        if (i0 + k * 32 + lane >= end) break;
+        const uint32_t d = (key[k] >> shift) & (kSortBins - 1);
+        const uint32_t dst = start[d] + mine[d] + off[k];
+        kout[dst] = key[k];
+        pout[dst] = from[k];
       }
-      __syncwarp();
     }
-    // the next pass (or the run boundaries) reads what every block wrote
-    __threadfence();
+    // the next pass (or the run boundaries) reads what every block wrote (the
+    // cluster's barrier releases and acquires global memory too)
     cluster.sync();
   }
 
   const uint32_t* keys = p.keys[(p.passes + 1) & 1];
-  for (long long i = static_cast<long long>(rank) * kSortThreads + tid; i < p.n;
-       i += static_cast<long long>(nb) * kSortThreads) {
+  for (uint32_t i = rank * kSortThreads + tid; i < n; i += nb * kSortThreads) {
     const uint32_t k = keys[i];
-    if (k >= p.vocab) continue;
-    if (i == 0 || keys[i - 1] != k) p.lo[k] = static_cast<uint32_t>(i);
-    if (i == p.n - 1 || keys[i + 1] != k) p.hi[k] = static_cast<uint32_t>(i + 1);
+    if (k >= vocab) continue;
+    if (i == 0 || keys[i - 1] != k) p.lo[k] = i;
+    if (i == n - 1 || keys[i + 1] != k) p.hi[k] = i + 1;
+  }
+  cluster.sync();
+  // The long runs, cut into pieces of at most kEmbedPiece positions.  Their
+  // order in the lists is no one's concern: a piece's sum goes to the row, or
+  // to a slot from which the run's slots are added in order.
+  for (uint32_t i = rank * kSortThreads + tid; i < n; i += nb * kSortThreads) {
+    const uint32_t k = keys[i];
+    if (k >= vocab || (i < n - 1 && keys[i + 1] == k)) continue;
+    const uint32_t lo = p.lo[k], len = i + 1 - lo;
+    if (len <= kEmbedLongRun) continue;
+    const uint32_t pieces = (len + kEmbedPiece - 1) / kEmbedPiece;
+    uint32_t slot = 0;
+    if (pieces > 1) {
+      slot = atomicAdd(&p.counts->slots, pieces);
+      p.joins[atomicAdd(&p.counts->joins, 1u)] = make_uint4(k, slot, slot + pieces, 0);
+    }
+    const uint32_t item = atomicAdd(&p.counts->items, pieces);
+    for (uint32_t j = 0; j < pieces; ++j)
+      p.items[item + j] = make_uint4(k, lo + j * kEmbedPiece, min(i + 1, lo + (j + 1) * kEmbedPiece),
+                                     pieces > 1 ? slot + j : kEmbedNoSlot);
   }
 }
 
 // ---------------------------------------------------------------- gradient
-// The columns a lane sums: 8 adjacent ones, or 4 that lie 32 apart.
-template <bool VEC>
-struct Acc {
-  static constexpr int N = VEC ? 8 : 4;
-  float v[N];
+// The columns of one row that a lane sums.
+struct Sums {
+  float v[kSumUnits][8];
 };
 
 template <typename D, bool VEC>
-__device__ __forceinline__ void add_row(const D* row, int c0, int lane, int dim, Acc<VEC>& a) {
-  if constexpr (VEC) {
-    const int c = c0 + lane * 8;
-    if (c < dim) {
-      float v[8];
-      load8(row + c, v);
+struct RowPiece {
+  Raw8<D> raw[kSumUnits];
+  float f[VEC ? 1 : kSumUnits][8];
+  __device__ __forceinline__ void load(const D* row, int dim, int c0, int lpr, int l) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) a.v[k] += v[k];
-    }
-  } else {
+    for (int u = 0; u < kSumUnits; ++u) {
+      if constexpr (VEC) {
+        const int c = seg_col<true>(c0, lpr, l, u, 0);
+        if (c < dim) raw[u] = load_raw8(row + c);
+      } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k * 32 + lane;
-      if (c < dim) a.v[k] += to_f32(row[c]);
+        for (int e = 0; e < 8; ++e) {
+          const int c = seg_col<false>(c0, lpr, l, u, e);
+          f[u][e] = c < dim ? to_f32(row[c]) : 0.f;
+        }
+      }
     }
+  }
+  __device__ __forceinline__ void add_to(Sums& a, int dim, int c0, int lpr, int l) const {
+#pragma unroll
+    for (int u = 0; u < kSumUnits; ++u) {
+      if constexpr (VEC) {
+        if (seg_col<true>(c0, lpr, l, u, 0) >= dim) break;
+        float v[8];
+        unpack8(raw[u], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a.v[u][e] += v[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a.v[u][e] += f[u][e];
+      }
+    }
+  }
+};
+
+// a += rows at(lo), ..., at(hi - 1), in that order; AHEAD of them are loaded
+// before the first is added.
+template <typename D, bool VEC, int AHEAD, typename At>
+__device__ __forceinline__ void add_rows(uint32_t lo, uint32_t hi, int dim, int c0, int lpr, int l, Sums& a, At at) {
+  uint32_t i = lo;
+  for (; i + AHEAD <= hi; i += AHEAD) {
+    const D* row[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) row[k] = at(i + k);
+    RowPiece<D, VEC> r[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) r[k].load(row[k], dim, c0, lpr, l);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) r[k].add_to(a, dim, c0, lpr, l);
+  }
+  for (; i < hi; ++i) {
+    RowPiece<D, VEC> r;
+    r.load(at(i), dim, c0, lpr, l);
+    r.add_to(a, dim, c0, lpr, l);
   }
 }
 
-// a += the rows at sorted positions [lo, hi), in order.
-template <typename D, bool VEC>
-__device__ __forceinline__ void add_run(const EmbedGradParams& p, const uint32_t* pos, uint32_t lo, uint32_t hi,
-                                        int c0, int lane, Acc<VEC>& a) {
-  const D* dout = static_cast<const D*>(p.dout);
-  for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
-    const uint32_t mine = i0 + lane < hi ? pos[i0 + lane] : 0;
-    const int cnt = min(32u, hi - i0);
-#pragma unroll 4
-    for (int j = 0; j < cnt; ++j) {
-      const uint32_t t = __shfl_sync(0xffffffffu, mine, j);
-      add_row<D, VEC>(dout + static_cast<long long>(t) * p.dout_ld, c0, lane, p.dim, a);
-    }
-  }
-}
-
-// One warp per (whole chunk of a long run, column segment).
-template <typename D, bool VEC>
-__global__ void __launch_bounds__(kEmbThreads) embedding_chunk_kernel(const EmbedGradParams p, int nseg) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const long long task = static_cast<long long>(blockIdx.x) * kEmbWarps + (threadIdx.x >> 5);
-  const long long chunk = task / nseg;
-  if ((chunk + 1) * kEmbedChunk > p.n) return;
-  const int lane = threadIdx.x & 31;
-  const int c0 = static_cast<int>(task - chunk * nseg) * kSegCols<VEC>;
-  const uint32_t* keys = p.keys[(p.passes + 1) & 1];
-  const uint32_t* pos = p.pos[(p.passes + 1) & 1];
-  const uint32_t lo = static_cast<uint32_t>(chunk * kEmbedChunk), hi = lo + kEmbedChunk;
-  const uint32_t k = keys[lo];
-  if (k >= p.vocab || keys[hi - 1] != k || p.hi[k] - p.lo[k] <= kEmbedLongRun) return;
-  Acc<VEC> a = {};
-  add_run<D, VEC>(p, pos, lo, hi, c0, lane, a);
-  float* out = p.partial + chunk * p.dim;
-  if constexpr (VEC) {
-    const int c = c0 + lane * 8;
-    if (c < p.dim) store8(out + c, a.v);
-  } else {
+// grad row's columns <- (old +) scale * sums
+template <typename G, bool VEC>
+__device__ __forceinline__ void write_row(const EmbedGradParams& p, G* out, int c0, int lpr, int l, const Sums& a) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + j * 32 + lane;
-      if (c < p.dim) out[c] = a.v[j];
-    }
-  }
-}
-
-// One warp per (row of the table, column segment).
-template <typename D, typename G, bool VEC>
-__global__ void __launch_bounds__(kEmbThreads) embedding_row_kernel(const EmbedGradParams p, int nseg) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const long long task = static_cast<long long>(blockIdx.x) * kEmbWarps + (threadIdx.x >> 5);
-  const long long v = task / nseg;
-  if (v >= p.vocab) return;
-  const int lane = threadIdx.x & 31;
-  const int c0 = static_cast<int>(task - v * nseg) * kSegCols<VEC>;
-  const uint32_t lo = p.lo[v], hi = p.hi[v];
-  if (lo == hi && p.accumulate) return;
-  const uint32_t* pos = p.pos[(p.passes + 1) & 1];
-  Acc<VEC> a = {};
-  if (hi - lo <= kEmbedLongRun) {
-    add_run<D, VEC>(p, pos, lo, hi, c0, lane, a);
-  } else {
-    const uint32_t first = (lo + kEmbedChunk - 1) / kEmbedChunk, last = hi / kEmbedChunk;   // whole chunks
-    add_run<D, VEC>(p, pos, lo, first * kEmbedChunk, c0, lane, a);
-#pragma unroll 8
-    for (uint32_t c = first; c < last; ++c)
-      add_row<float, VEC>(p.partial + static_cast<long long>(c) * p.dim, c0, lane, p.dim, a);
-    add_run<D, VEC>(p, pos, last * kEmbedChunk, hi, c0, lane, a);
-  }
-  G* out = static_cast<G*>(p.grad) + v * p.dim;
-  if constexpr (VEC) {
-    const int c = c0 + lane * 8;
-    if (c < p.dim) {
+  for (int u = 0; u < kSumUnits; ++u) {
+    if constexpr (VEC) {
+      const int c = seg_col<true>(c0, lpr, l, u, 0);
+      if (c >= p.dim) break;
       float o[8] = {};
       if (p.accumulate) load8(out + c, o);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = fmaf(p.scale, a.v[k], o[k]);
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(p.scale, a.v[u][e], o[e]);
       store8(out + c, o);
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k * 32 + lane;
-      if (c < p.dim) out[c] = from_f32<G>(fmaf(p.scale, a.v[k], p.accumulate ? to_f32(out[c]) : 0.f));
+      for (int e = 0; e < 8; ++e) {
+        const int c = seg_col<false>(c0, lpr, l, u, e);
+        if (c < p.dim) out[c] = from_f32<G>(fmaf(p.scale, a.v[u][e], p.accumulate ? to_f32(out[c]) : 0.f));
+      }
     }
   }
 }
 
+// Sum of the block's warps, in order, in warp 0; every warp calls it.
+__device__ __forceinline__ void block_sum(Sums& a, float (&part)[kEmbWarps][kSumUnits * 8][32]) {
+  const int lane = threadIdx.x, warp = threadIdx.y;
+#pragma unroll
+  for (int i = 0; i < kSumUnits * 8; ++i) part[warp][i][lane] = a.v[i / 8][i % 8];
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < kSumUnits * 8; ++i) {
+      float v = part[0][i][lane];
+#pragma unroll
+      for (int w = 1; w < kEmbWarps; ++w) v += part[w][i][lane];
+      a.v[i / 8][i % 8] = v;
+    }
+  }
+  __syncthreads();
+}
+
+// Pieces of long runs (JOIN: the slots of runs of several pieces): a block per
+// piece and 512 columns, over a list whose length only the device knows.  Each
+// warp adds a contiguous eighth of the terms.
+template <typename D, typename G, bool VEC, bool JOIN>
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_long_kernel(const EmbedGradParams p, int segs) {
+  __shared__ float part[kEmbWarps][kSumUnits * 8][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint32_t* pos = p.pos[(p.passes + 1) & 1];
+  const int lane = threadIdx.x, warp = threadIdx.y;
+  const uint32_t count = JOIN ? p.counts->joins : p.counts->items;
+  for (unsigned long long it = blockIdx.x; it < static_cast<unsigned long long>(count) * segs; it += gridDim.x) {
+    const uint32_t i = static_cast<uint32_t>(it / segs);
+    const int c0 = static_cast<int>(it - static_cast<unsigned long long>(i) * segs) * (32 * 8 * kSumUnits);
+    const uint4 w = JOIN ? p.joins[i] : p.items[i];
+    const uint32_t len = w.z - w.y, b = w.y + len * warp / kEmbWarps, e = w.y + len * (warp + 1) / kEmbWarps;
+    Sums a = {};
+    if constexpr (JOIN)
+      add_rows<float, VEC, VEC ? 4 : 1>(b, e, p.dim, c0, 32, lane, a,
+                                        [&](uint32_t k) { return p.partial + static_cast<long long>(k) * p.dim; });
+    else
+      add_rows<D, VEC, VEC ? 4 : 1>(b, e, p.dim, c0, 32, lane, a,
+                                    [&](uint32_t k) { return static_cast<const D*>(p.dout) + pos[k] * p.dout_ld; });
+    block_sum(a, part);
+    if (warp != 0) continue;
+    if (!JOIN && w.w != kEmbedNoSlot) {
+      float* out = p.partial + static_cast<long long>(w.w) * p.dim;
+#pragma unroll
+      for (int u = 0; u < kSumUnits; ++u) {
+        if constexpr (VEC) {
+          const int c = seg_col<true>(c0, 32, lane, u, 0);
+          if (c < p.dim) store8(out + c, a.v[u]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int c = seg_col<false>(c0, 32, lane, u, q);
+            if (c < p.dim) out[c] = a.v[u][q];
+          }
+        }
+      }
+    } else {
+      write_row<G, VEC>(p, static_cast<G*>(p.grad) + static_cast<long long>(w.x) * p.dim, c0, 32, lane, a);
+    }
+  }
+}
+
+// The other rows of the table.  Most have no token or a few: the kernel is
+// bound by writing them, so it keeps to 64 registers and full blocks.
+template <typename D, typename G, bool VEC>
+__global__ void __launch_bounds__(32 * kEmbWarps, 4) embedding_row_kernel(const EmbedGradParams p, const EmbedShape sh) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const LaneRow w = lane_row(sh);
+  if (w.row >= p.vocab || w.c0 >= p.dim) return;
+  const uint32_t lo = p.lo[w.row], hi = p.hi[w.row];
+  if ((lo == hi && p.accumulate) || hi - lo > kEmbedLongRun) return;
+  const uint32_t* pos = p.pos[(p.passes + 1) & 1];
+  Sums a = {};
+  add_rows<D, VEC, VEC && sizeof(D) == 2 ? 2 : 1>(
+      lo, hi, p.dim, w.c0, sh.lpr, w.l, a,
+      [&](uint32_t i) { return static_cast<const D*>(p.dout) + pos[i] * p.dout_ld; });
+  write_row<G, VEC>(p, static_cast<G*>(p.grad) + w.row * p.dim, w.c0, sh.lpr, w.l, a);
+}
+
 // ---------------------------------------------------------------- launchers
-template <bool VEC>
-static int segments(int dim) { return (dim + kSegCols<VEC> - 1) / kSegCols<VEC>; }
-static dim3 warp_grid(long long tasks) { return dim3(static_cast<unsigned>((tasks + kEmbWarps - 1) / kEmbWarps)); }
+namespace {
+struct EmbedLaunch {
+  EmbedShape shape;
+  dim3 grid, block;
+};
+EmbedLaunch embed_launch(long long rows, int dim, int units) {
+  EmbedLaunch l;
+  l.shape.lpr = 32;
+  while (l.shape.lpr > 1 && dim <= l.shape.lpr / 2 * 8 * units) l.shape.lpr /= 2;
+  l.shape.cols = 32 * 8 * units;
+  const int segs = (dim + l.shape.cols - 1) / l.shape.cols;
+  l.shape.wx = 1;
+  while (l.shape.wx < kEmbWarps && l.shape.wx < segs) l.shape.wx *= 2;
+  l.block = dim3(32, l.shape.wx, kEmbWarps / l.shape.wx);
+  const long long per = static_cast<long long>(l.block.z) * (32 / l.shape.lpr);
+  l.grid = dim3(static_cast<unsigned>((rows + per - 1) / per), (segs + l.shape.wx - 1) / l.shape.wx);
+  return l;
+}
+}  // namespace
 
 template <typename T, typename O, bool VEC>
 static cudaError_t embedding_typed(const EmbedParams& p, cudaStream_t s) {
-  const int nseg = segments<VEC>(p.dim);
-  return launch_pdl(embedding_kernel<T, O, VEC>, warp_grid(p.n * nseg), dim3(kEmbThreads), 0, s, p, nseg);
+  const EmbedLaunch l = embed_launch(p.n, p.dim, kSegUnits);
+  return launch_pdl(embedding_kernel<T, O, VEC>, l.grid, l.block, 0, s, p, l.shape);
 }
 cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s) {
   using F = cudaError_t (*)(const EmbedParams&, cudaStream_t);
@@ -350,17 +513,49 @@ cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s) {
   return table[p.table_bf16][p.out_bf16][p.vec](p, s);
 }
 
+// Blocks of the sort's cluster: enough that a lane has few keys, and that
+// clearing the runs of a large table is shared.  16 where the GPU can place
+// such a cluster (beyond the portable 8).
+static cudaError_t sort_limit(int* limit) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*limit = known[dev].load(std::memory_order_relaxed)) != 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  *limit = 8;
+  if (cudaOccupancyMaxActiveClusters(&clusters, embedding_sort_kernel, &cfg) == cudaSuccess && clusters > 0) *limit = 16;
+  else cudaGetLastError();
+  if (dev < 64) known[dev].store(*limit, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int limit = 8;
+  if (e == cudaSuccess) e = sort_limit(&limit);
   if (e != cudaSuccess) return e;
+  const long long want = std::max((p.n + 2047) / 2048, p.vocab / 16384);
+  unsigned nb = 1;
+  while (static_cast<int>(nb) < limit && nb < want) nb *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSortCluster);
+  cfg.gridDim = dim3(nb);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = kSortSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSortCluster;
+  attr[0].val.clusterDim.x = nb;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -370,22 +565,29 @@ cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, embedding_sort_kernel, p);
 }
 
-template <typename D, bool VEC>
-static cudaError_t chunks_typed(const EmbedGradParams& p, cudaStream_t s) {
-  const int nseg = segments<VEC>(p.dim);
-  return launch_pdl(embedding_chunk_kernel<D, VEC>, warp_grid(p.n / kEmbedChunk * nseg), dim3(kEmbThreads), 0, s, p,
-                    nseg);
-}
-cudaError_t launch_embedding_chunks(const EmbedGradParams& p, cudaStream_t s) {
-  using B = __nv_bfloat16;
-  if (p.dout_bf16) return p.vec ? chunks_typed<B, true>(p, s) : chunks_typed<B, false>(p, s);
-  return p.vec ? chunks_typed<float, true>(p, s) : chunks_typed<float, false>(p, s);
-}
-
 template <typename D, typename G, bool VEC>
 static cudaError_t rows_typed(const EmbedGradParams& p, cudaStream_t s) {
-  const int nseg = segments<VEC>(p.dim);
-  return launch_pdl(embedding_row_kernel<D, G, VEC>, warp_grid(p.vocab * nseg), dim3(kEmbThreads), 0, s, p, nseg);
+  const EmbedLaunch l = embed_launch(p.vocab, p.dim, kSumUnits);
+  return launch_pdl(embedding_row_kernel<D, G, VEC>, l.grid, l.block, 0, s, p, l.shape);
+}
+template <typename D, typename G, bool VEC>
+static cudaError_t long_typed(const EmbedGradParams& p, bool join, cudaStream_t s) {
+  constexpr int kCols = 32 * 8 * kSumUnits;
+  const int segs = (p.dim + kCols - 1) / kCols;
+  // at most n / (kEmbedLongRun + 1) runs are long, n / (kEmbedPiece + 1) of several pieces
+  const long long most = (join ? p.n / (kEmbedPiece + 1) : embed_max_items(p.n)) * segs;
+  const dim3 grid(static_cast<unsigned>(std::min<long long>(most, 2 * p.sms)));
+  if (join) return launch_pdl(embedding_long_kernel<D, G, VEC, true>, grid, dim3(32, kEmbWarps), 0, s, p, segs);
+  return launch_pdl(embedding_long_kernel<D, G, VEC, false>, grid, dim3(32, kEmbWarps), 0, s, p, segs);
+}
+cudaError_t launch_embedding_long(const EmbedGradParams& p, bool join, cudaStream_t s) {
+  using F = cudaError_t (*)(const EmbedGradParams&, bool, cudaStream_t);
+  using B = __nv_bfloat16;
+  static const F table[2][2][2] = {
+      {{long_typed<float, float, false>, long_typed<float, float, true>},
+       {long_typed<float, B, false>, long_typed<float, B, true>}},
+      {{long_typed<B, float, false>, long_typed<B, float, true>}, {long_typed<B, B, false>, long_typed<B, B, true>}}};
+  return table[p.dout_bf16][p.grad_bf16][p.vec](p, join, s);
 }
 cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s) {
   using F = cudaError_t (*)(const EmbedGradParams&, cudaStream_t);
