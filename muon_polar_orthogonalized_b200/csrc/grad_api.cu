@@ -83,17 +83,18 @@ muon_status check_embedding(int64_t vocab, int64_t dim, int64_t n, int32_t ids_b
 }
 
 struct EmbedWs {
-  size_t keys, runs, items, joins, partial, total;
+  size_t keys, runs, shorts, items, joins, partial, total;
 };
 EmbedWs embed_ws(int64_t vocab, int64_t dim, int64_t n) {
   EmbedWs w;
   w.keys = up256(static_cast<size_t>(n) * 4);
   w.runs = up256(static_cast<size_t>(vocab) * 4);
+  w.shorts = up256(static_cast<size_t>(std::min(n, vocab)) * 16);
   w.items = up256(static_cast<size_t>(embed_max_items(n)) * 16);
   w.joins = up256(static_cast<size_t>(n / (kEmbedPiece + 1)) * 16);
   // a run of several pieces has less than two slots per kEmbedPiece positions
   w.partial = up256(static_cast<size_t>(n / kEmbedPiece + n / (kEmbedPiece + 1)) * dim * 4);
-  w.total = 256 + 5 * w.keys + 2 * w.runs + w.items + w.joins + w.partial;
+  w.total = 256 + 5 * w.keys + w.runs + w.shorts + w.items + w.joins + w.partial;
   return w;
 }
 
@@ -251,11 +252,10 @@ muon_status muon_embedding_grad(const void* dout, int32_t dout_dtype, int64_t do
       b += bytes;
       return r;
     };
-    for (int i = 0; i < 2; ++i) p.keys[i] = reinterpret_cast<uint32_t*>(take(w.keys));
-    for (int i = 0; i < 2; ++i) p.pos[i] = reinterpret_cast<uint32_t*>(take(w.keys));
+    for (int i = 0; i < 2; ++i) p.sorted[i] = reinterpret_cast<uint2*>(take(2 * w.keys));
     p.offset = reinterpret_cast<uint32_t*>(take(w.keys));
-    p.lo = reinterpret_cast<uint32_t*>(take(w.runs));
-    p.hi = reinterpret_cast<uint32_t*>(take(w.runs));
+    p.first = reinterpret_cast<uint32_t*>(take(w.runs));
+    p.shorts = reinterpret_cast<uint4*>(take(w.shorts));
     p.counts = reinterpret_cast<EmbedCounts*>(p.status + 4);
     p.items = reinterpret_cast<uint4*>(take(w.items));
     p.joins = reinterpret_cast<uint4*>(take(w.joins));
@@ -269,14 +269,11 @@ muon_status muon_embedding_grad(const void* dout, int32_t dout_dtype, int64_t do
     st = launched(api_timed_launch(K_EMBED_SORT, s, [&] { return launch_embedding_sort(p, s); }),
                   "embedding sort launch");
     if (st != MUON_OK) return st;
-    for (int join = 0; join < 2; ++join) {
-      if (n <= (join ? kEmbedPiece : kEmbedLongRun)) break;   // no run is that long
-      st = launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_long(p, join != 0, s); }),
-                    "embedding long-run launch");
-      if (st != MUON_OK) return st;
-    }
-    return launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_rows(p, s); }),
-                    "embedding row launch");
+    st = launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_rows(p, s); }),
+                  "embedding row launch");
+    if (st != MUON_OK || n <= kEmbedPiece) return st;   // no run has several pieces
+    return launched(api_timed_launch(K_EMBED_GRAD, s, [&] { return launch_embedding_join(p, s); }),
+                    "embedding join launch");
   });
 }
 

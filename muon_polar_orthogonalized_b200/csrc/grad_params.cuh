@@ -26,7 +26,7 @@ constexpr uint32_t kEmbedNoSlot = 0xffffffffu;
 // Most pieces that n positions can make.
 inline long long embed_max_items(long long n) { return n / kEmbedPiece + n / (kEmbedLongRun + 1); }
 struct EmbedCounts {
-  uint32_t items, slots, joins;
+  uint32_t shorts, items, slots, joins;
 };
 
 struct EmbedGradParams {
@@ -40,13 +40,12 @@ struct EmbedGradParams {
   float scale;
   // workspace
   unsigned int* status;   // word 0: cleared by every call (muon_query_status)
-  uint32_t* keys[2];   // [n] sort buffers: ids (vocab for "no token") ...
-  uint32_t* pos[2];    // ... and the positions they come from
-  uint32_t* lo;        // [vocab] first and one past the last sorted position of each id
-  uint32_t* hi;
+  uint2* sorted[2];    // [n] sort buffers: (id, vocab for "no token"; position it comes from)
+  uint32_t* first;     // [vocab] 1 + first sorted position of each id, 0 where it does not occur
   uint32_t* offset;    // [n] a key's offset within its warp and digit
   EmbedCounts* counts;
-  uint4* items;        // pieces: (id, first and one past the last sorted position, slot or kEmbedNoSlot)
+  uint4* shorts;       // short runs: (id, first and one past the last sorted position, -)
+  uint4* items;        // pieces of long runs: (id, first and one past the last sorted position, slot or kEmbedNoSlot)
   uint4* joins;        // runs of several pieces: (id, first and one past the last slot, -)
   float* partial;      // [slot][dim] sums of the pieces of such runs
   int passes;          // of the radix sort, 9 bits each
@@ -113,8 +112,8 @@ struct alignas(64) WeightGradTc {
 
 cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s);
 cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s);
-cudaError_t launch_embedding_long(const EmbedGradParams& p, bool join, cudaStream_t s);
 cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s);
+cudaError_t launch_embedding_join(const EmbedGradParams& p, cudaStream_t s);
 cudaError_t launch_layer_norm(const NormParams& p, cudaStream_t s);
 cudaError_t launch_layer_norm_grad(const NormParams& p, cudaStream_t s);
 cudaError_t launch_layer_norm_columns(const NormParams& p, cudaStream_t s);

@@ -6,13 +6,15 @@
 //                   in fp32, in an order that depends on the ids alone
 //
 // Lookup and gradient stream: their floor is the rows read and written.  The
-// gradient never adds into memory from several threads: the ids are sorted,
-// so each row of E has one run of sorted positions [lo, hi), and one warp per
-// row and column segment sums the run in order and writes the row once (an
-// empty run writes zeros, or nothing when accumulating).  Frequent tokens
+// gradient never adds into memory from several threads: the ids are sorted, so
+// that each row of E has one run of sorted positions, and a warp per run and
+// row piece adds the run in order and writes the row once.  Frequent tokens
 // have runs of thousands of positions; runs longer than kEmbedLongRun are cut
 // into pieces of kEmbedPiece positions, a block sums each piece (eight warps, an
 // eighth each), and the pieces of a run are added in order by another block.
+// Rows without a token are written as zeros by one warp of each block, beside
+// the warps that add.  (Writing zeros everywhere beside the sort instead made
+// the sort, which waits for L2, four times as long.)
 //
 // The sort is a least-significant-digit radix sort (stable, so positions stay
 // ascending within an id) by ONE thread-block cluster: the blocks exchange
@@ -28,6 +30,7 @@
 
 #include "grad_params.cuh"
 #include "pdl.cuh"
+#include "sm100.cuh"
 #include "vec8.cuh"
 
 namespace muon {
@@ -39,7 +42,7 @@ namespace cg = cooperative_groups;
 // them out in groups of `lpr` lanes, a row each.  No index is divided.
 constexpr int kEmbWarps = 8;
 constexpr int kSegUnits = 4;    // 8-column units per lane: lookup
-constexpr int kSumUnits = 2;    // and gradient, which holds sums and several rows' units in registers
+constexpr int kSumUnits = 1;    // gradient, which holds sums and several rows' units in registers
 struct EmbedShape {
   int lpr;        // lanes per row: 32, or fewer for rows of at most lpr * 8 * units columns
   int wx;
@@ -142,7 +145,7 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t act, uint32_t d) {
 // memory.  Placing, a key goes to the start of its digit, plus what earlier
 // blocks and warps hold of it, plus its offset.
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const EmbedGradParams p) {
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(128) uint32_t sm[];
   uint32_t* hist = sm;                                  // [warp][bin]
   uint32_t* total = sm + kSortWarps * kSortBins;        // [bin] of this block, read by the cluster
   uint32_t* start = total + kSortBins;                  // [bin] of this block's first key
@@ -156,35 +159,31 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
 
   if (rank == 0 && tid == 0) {
     *p.status = 0;
-    p.counts->items = p.counts->slots = p.counts->joins = 0;
+    p.counts->shorts = p.counts->items = p.counts->slots = p.counts->joins = 0;
   }
-  // no id has been seen yet (the arrays are padded to whole 16-byte units)
-  for (uint32_t v = rank * kSortThreads + tid; v < (vocab + 3) / 4; v += nb * kSortThreads) {
-    reinterpret_cast<uint4*>(p.lo)[v] = make_uint4(0, 0, 0, 0);
-    reinterpret_cast<uint4*>(p.hi)[v] = make_uint4(0, 0, 0, 0);
-  }
+  // no id has been seen yet (the array is padded to whole 16-byte units)
+  for (uint32_t v = rank * kSortThreads + tid; v < (vocab + 3) / 4; v += nb * kSortThreads)
+    reinterpret_cast<uint4*>(p.first)[v] = make_uint4(0, 0, 0, 0);
   const uint32_t warps = nb * kSortWarps;
   const uint32_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
   const uint32_t begin = min(n, (rank * kSortWarps + warp) * per), end = min(n, begin + per);
 
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * kSortBits;
-    const uint32_t* kin = p.keys[(pass + 1) & 1];
-    const uint32_t* pin = p.pos[(pass + 1) & 1];
-    uint32_t* kout = p.keys[pass & 1];
-    uint32_t* pout = p.pos[pass & 1];
-    // kSortKeys keys of this lane from position i0 on, 32 positions apart
-    auto load_keys = [&](uint32_t i0, uint32_t (&key)[kSortKeys]) {
+    const uint2* in = p.sorted[(pass + 1) & 1];
+    uint2* out = p.sorted[pass & 1];
+    // kSortKeys (key, position)s of this lane from position i0 on, 32 apart
+    auto load_keys = [&](uint32_t i0, uint2 (&key)[kSortKeys]) {
 #pragma unroll
       for (int k = 0; k < kSortKeys; ++k) {
         const uint32_t i = i0 + k * 32 + lane;
-        key[k] = 0;
+        key[k] = make_uint2(0, i);
         if (i < end) {
           if (pass) {
-            key[k] = kin[i];
+            key[k] = in[i];
           } else {
             const long long row = token_row(p.ids, p.ids64, i, p.vocab);
-            key[k] = row < 0 ? vocab : static_cast<uint32_t>(row);
+            key[k].x = row < 0 ? vocab : static_cast<uint32_t>(row);
           }
         }
       }
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
     for (int b = 0; b < kSortBins; b += 128) *reinterpret_cast<uint4*>(mine + b + lane * 4) = make_uint4(0, 0, 0, 0);
     __syncwarp();
     for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortKeys) {
-      uint32_t key[kSortKeys];
+      uint2 key[kSortKeys];
       load_keys(i0, key);
 #pragma unroll
       for (int k = 0; k < kSortKeys; ++k) {
@@ -202,7 +201,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
         const uint32_t i = i0 + k * 32 + lane;
         const uint32_t act = __ballot_sync(0xffffffffu, i < end);
         if (i < end) {
-          const uint32_t d = (key[k] >> shift) & (kSortBins - 1);
+          const uint32_t d = (key[k].x >> shift) & (kSortBins - 1);
           const uint32_t peers = same_digit(act, d);
           const uint32_t rk = __popc(peers & ((1u << lane) - 1)), so_far = mine[d];
           p.offset[i] = so_far + rk;
@@ -232,9 +231,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
       cluster.sync();
       if (tid < kSortBins) {
         all = 0;
-#pragma unroll 4
-        for (uint32_t r = 0; r < nb; ++r) {
-          const uint32_t c = cluster.map_shared_rank(total, r)[tid];
+#pragma unroll
+        for (uint32_t r = 0; r < 16; ++r) {
+          const uint32_t c = r < nb ? cluster.map_shared_rank(total, r)[tid] : 0;
           if (r < rank) before += c;
           all += c;
         }
@@ -256,21 +255,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
     }
     __syncthreads();
     for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortKeys) {
-      uint32_t key[kSortKeys], from[kSortKeys], off[kSortKeys];
+      uint2 key[kSortKeys];
+      uint32_t off[kSortKeys];
       load_keys(i0, key);
 #pragma unroll
       for (int k = 0; k < kSortKeys; ++k) {
         const uint32_t i = i0 + k * 32 + lane;
-        from[k] = pass && i < end ? pin[i] : i;
         off[k] = i < end ? p.offset[i] : 0;
       }
 #pragma unroll
       for (int k = 0; k < kSortKeys; ++k) {
         if (i0 + k * 32 + lane >= end) break;
-        const uint32_t d = (key[k] >> shift) & (kSortBins - 1);
-        const uint32_t dst = start[d] + mine[d] + off[k];
-        kout[dst] = key[k];
-        pout[dst] = from[k];
+        const uint32_t d = (key[k].x >> shift) & (kSortBins - 1);
+        out[start[d] + mine[d] + off[k]] = key[k];
       }
     }
     // the next pass (or the run boundaries) reads what every block wrote (the
@@ -278,48 +275,72 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
     cluster.sync();
   }
 
-  const uint32_t* keys = p.keys[(p.passes + 1) & 1];
-  for (uint32_t i = rank * kSortThreads + tid; i < n; i += nb * kSortThreads) {
-    const uint32_t k = keys[i];
-    if (k >= vocab) continue;
-    if (i == 0 || keys[i - 1] != k) p.lo[k] = i;
-    if (i == n - 1 || keys[i + 1] != k) p.hi[k] = i + 1;
+  // Where runs start (kept per id), then, at their ends, the lists of runs.
+  const uint2* sorted = p.sorted[(p.passes + 1) & 1];
+  const uint32_t stride = nb * kSortThreads;
+  for (uint32_t i0 = rank * kSortThreads + tid; i0 < n; i0 += 4 * stride) {
+    uint32_t k[4], left[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t i = i0 + j * stride;
+      k[j] = i < n ? sorted[i].x : vocab;
+      left[j] = i < n && i > 0 ? sorted[i - 1].x : vocab;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (k[j] < vocab && k[j] != left[j]) p.first[k[j]] = i0 + j * stride + 1;
   }
   cluster.sync();
-  // The long runs, cut into pieces of at most kEmbedPiece positions.  Their
-  // order in the lists is no one's concern: a piece's sum goes to the row, or
-  // to a slot from which the run's slots are added in order.
-  for (uint32_t i = rank * kSortThreads + tid; i < n; i += nb * kSortThreads) {
-    const uint32_t k = keys[i];
-    if (k >= vocab || (i < n - 1 && keys[i + 1] == k)) continue;
-    const uint32_t lo = p.lo[k], len = i + 1 - lo;
-    if (len <= kEmbedLongRun) continue;
-    const uint32_t pieces = (len + kEmbedPiece - 1) / kEmbedPiece;
-    uint32_t slot = 0;
-    if (pieces > 1) {
-      slot = atomicAdd(&p.counts->slots, pieces);
-      p.joins[atomicAdd(&p.counts->joins, 1u)] = make_uint4(k, slot, slot + pieces, 0);
+  // The order of the entries is no one's concern: a run's sum goes to its row,
+  // or, for long runs in pieces of at most kEmbedPiece positions, to slots from
+  // which it is added in order.
+  for (uint32_t i0 = rank * kSortThreads + tid; i0 < n; i0 += 4 * stride) {
+    uint32_t k[4], right[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t i = i0 + j * stride;
+      k[j] = i < n ? sorted[i].x : vocab;
+      right[j] = i < n - 1 ? sorted[i + 1].x : vocab;
+      if (k[j] == right[j]) k[j] = vocab;   // not a run's end
     }
-    const uint32_t item = atomicAdd(&p.counts->items, pieces);
-    for (uint32_t j = 0; j < pieces; ++j)
-      p.items[item + j] = make_uint4(k, lo + j * kEmbedPiece, min(i + 1, lo + (j + 1) * kEmbedPiece),
-                                     pieces > 1 ? slot + j : kEmbedNoSlot);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lo[j] = k[j] < vocab ? p.first[k[j]] - 1 : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (k[j] >= vocab) continue;
+      const uint32_t hi = i0 + j * stride + 1, len = hi - lo[j];
+      if (len <= kEmbedLongRun) {
+        p.shorts[atomicAdd(&p.counts->shorts, 1u)] = make_uint4(k[j], lo[j], hi, 0);
+        continue;
+      }
+      const uint32_t pieces = (len + kEmbedPiece - 1) / kEmbedPiece;
+      uint32_t slot = 0;
+      if (pieces > 1) {
+        slot = atomicAdd(&p.counts->slots, pieces);
+        p.joins[atomicAdd(&p.counts->joins, 1u)] = make_uint4(k[j], slot, slot + pieces, 0);
+      }
+      const uint32_t item = atomicAdd(&p.counts->items, pieces);
+      for (uint32_t q = 0; q < pieces; ++q)
+        p.items[item + q] = make_uint4(k[j], lo[j] + q * kEmbedPiece, min(hi, lo[j] + (q + 1) * kEmbedPiece),
+                                       pieces > 1 ? slot + q : kEmbedNoSlot);
+    }
   }
 }
 
 // ---------------------------------------------------------------- gradient
 // The columns of one row that a lane sums.
+template <int UNITS>
 struct Sums {
-  float v[kSumUnits][8];
+  float v[UNITS][8];
 };
 
-template <typename D, bool VEC>
+template <typename D, bool VEC, int UNITS>
 struct RowPiece {
-  Raw8<D> raw[kSumUnits];
-  float f[VEC ? 1 : kSumUnits][8];
+  Raw8<D> raw[UNITS];
+  float f[VEC ? 1 : UNITS][8];
   __device__ __forceinline__ void load(const D* row, int dim, int c0, int lpr, int l) {
 #pragma unroll
-    for (int u = 0; u < kSumUnits; ++u) {
+    for (int u = 0; u < UNITS; ++u) {
       if constexpr (VEC) {
         const int c = seg_col<true>(c0, lpr, l, u, 0);
         if (c < dim) raw[u] = load_raw8(row + c);
@@ -332,9 +353,9 @@ struct RowPiece {
       }
     }
   }
-  __device__ __forceinline__ void add_to(Sums& a, int dim, int c0, int lpr, int l) const {
+  __device__ __forceinline__ void add_to(Sums<UNITS>& a, int dim, int c0, int lpr, int l) const {
 #pragma unroll
-    for (int u = 0; u < kSumUnits; ++u) {
+    for (int u = 0; u < UNITS; ++u) {
       if constexpr (VEC) {
         if (seg_col<true>(c0, lpr, l, u, 0) >= dim) break;
         float v[8];
@@ -351,31 +372,31 @@ struct RowPiece {
 
 // a += rows at(lo), ..., at(hi - 1), in that order; AHEAD of them are loaded
 // before the first is added.
-template <typename D, bool VEC, int AHEAD, typename At>
-__device__ __forceinline__ void add_rows(uint32_t lo, uint32_t hi, int dim, int c0, int lpr, int l, Sums& a, At at) {
+template <typename D, bool VEC, int AHEAD, int UNITS, typename At>
+__device__ __forceinline__ void add_rows(uint32_t lo, uint32_t hi, int dim, int c0, int lpr, int l, Sums<UNITS>& a, At at) {
   uint32_t i = lo;
   for (; i + AHEAD <= hi; i += AHEAD) {
     const D* row[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) row[k] = at(i + k);
-    RowPiece<D, VEC> r[AHEAD];
+    RowPiece<D, VEC, UNITS> r[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) r[k].load(row[k], dim, c0, lpr, l);
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) r[k].add_to(a, dim, c0, lpr, l);
   }
   for (; i < hi; ++i) {
-    RowPiece<D, VEC> r;
+    RowPiece<D, VEC, UNITS> r;
     r.load(at(i), dim, c0, lpr, l);
     r.add_to(a, dim, c0, lpr, l);
   }
 }
 
 // grad row's columns <- (old +) scale * sums
-template <typename G, bool VEC>
-__device__ __forceinline__ void write_row(const EmbedGradParams& p, G* out, int c0, int lpr, int l, const Sums& a) {
+template <typename G, bool VEC, int UNITS>
+__device__ __forceinline__ void write_row(const EmbedGradParams& p, G* out, int c0, int lpr, int l, const Sums<UNITS>& a) {
 #pragma unroll
-  for (int u = 0; u < kSumUnits; ++u) {
+  for (int u = 0; u < UNITS; ++u) {
     if constexpr (VEC) {
       const int c = seg_col<true>(c0, lpr, l, u, 0);
       if (c >= p.dim) break;
@@ -394,12 +415,13 @@ __device__ __forceinline__ void write_row(const EmbedGradParams& p, G* out, int 
   }
 }
 
-// Sum of the block's warps, in order, in warp 0; every warp calls it.
-__device__ __forceinline__ void block_sum(Sums& a, float (&part)[kEmbWarps][kSumUnits * 8][32]) {
+// Sum of the block's adding warps, in order, in warp 0; every one calls it.
+__device__ __forceinline__ void adders_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEmbWarps) : "memory"); }
+__device__ __forceinline__ void block_sum(Sums<kSumUnits>& a, float (&part)[kEmbWarps][kSumUnits * 8][32]) {
   const int lane = threadIdx.x, warp = threadIdx.y;
 #pragma unroll
   for (int i = 0; i < kSumUnits * 8; ++i) part[warp][i][lane] = a.v[i / 8][i % 8];
-  __syncthreads();
+  adders_barrier();
   if (warp == 0) {
 #pragma unroll
     for (int i = 0; i < kSumUnits * 8; ++i) {
@@ -409,32 +431,29 @@ __device__ __forceinline__ void block_sum(Sums& a, float (&part)[kEmbWarps][kSum
       a.v[i / 8][i % 8] = v;
     }
   }
-  __syncthreads();
+  adders_barrier();
 }
 
-// Pieces of long runs (JOIN: the slots of runs of several pieces): a block per
-// piece and 512 columns, over a list whose length only the device knows.  Each
-// warp adds a contiguous eighth of the terms.
+// A block's share of a list of pieces (JOIN: of runs' slots), row piece by row
+// piece.  Each warp adds a contiguous eighth of the terms.
 template <typename D, typename G, bool VEC, bool JOIN>
-__global__ void __launch_bounds__(32 * kEmbWarps) embedding_long_kernel(const EmbedGradParams p, int segs) {
-  __shared__ float part[kEmbWarps][kSumUnits * 8][32];
-  pdl_launch_dependents();
-  pdl_wait();
-  const uint32_t* pos = p.pos[(p.passes + 1) & 1];
+__device__ __forceinline__ void add_long(const EmbedGradParams& p, uint32_t segs,
+                                         float (&part)[kEmbWarps][kSumUnits * 8][32]) {
+  const uint2* sorted = p.sorted[(p.passes + 1) & 1];
   const int lane = threadIdx.x, warp = threadIdx.y;
   const uint32_t count = JOIN ? p.counts->joins : p.counts->items;
   for (unsigned long long it = blockIdx.x; it < static_cast<unsigned long long>(count) * segs; it += gridDim.x) {
-    const uint32_t i = static_cast<uint32_t>(it / segs);
+    const uint32_t i = it <= 0xffffffffull ? static_cast<uint32_t>(it) / segs : static_cast<uint32_t>(it / segs);
     const int c0 = static_cast<int>(it - static_cast<unsigned long long>(i) * segs) * (32 * 8 * kSumUnits);
     const uint4 w = JOIN ? p.joins[i] : p.items[i];
     const uint32_t len = w.z - w.y, b = w.y + len * warp / kEmbWarps, e = w.y + len * (warp + 1) / kEmbWarps;
-    Sums a = {};
+    Sums<kSumUnits> a = {};
     if constexpr (JOIN)
-      add_rows<float, VEC, VEC ? 4 : 1>(b, e, p.dim, c0, 32, lane, a,
+      add_rows<float, VEC, VEC ? 4 : 2>(b, e, p.dim, c0, 32, lane, a,
                                         [&](uint32_t k) { return p.partial + static_cast<long long>(k) * p.dim; });
     else
-      add_rows<D, VEC, VEC ? 4 : 1>(b, e, p.dim, c0, 32, lane, a,
-                                    [&](uint32_t k) { return static_cast<const D*>(p.dout) + pos[k] * p.dout_ld; });
+      add_rows<D, VEC, VEC ? 4 : 2>(b, e, p.dim, c0, 32, lane, a,
+                                    [&](uint32_t k) { return static_cast<const D*>(p.dout) + sorted[k].y * p.dout_ld; });
     block_sum(a, part);
     if (warp != 0) continue;
     if (!JOIN && w.w != kEmbedNoSlot) {
@@ -458,22 +477,82 @@ __global__ void __launch_bounds__(32 * kEmbWarps) embedding_long_kernel(const Em
   }
 }
 
-// The other rows of the table.  Most have no token or a few: the kernel is
-// bound by writing them, so it keeps to 64 registers and full blocks.
+// Zeros in the rows that have no token, by the block's last warp: a lane per
+// row, bulk copies of a zeroed piece of shared memory (436 MB in 69 us; stores
+// from registers took 118), or the warp's stores where rows are not whole
+// 16-byte units.
+constexpr int kZeroBytes = 8192;
+template <typename G>
+__device__ __forceinline__ void fill_rows(const EmbedGradParams& p, const uint4* zeros) {
+  const int lane = threadIdx.x;
+  const long long bytes = static_cast<long long>(p.dim) * sizeof(G);
+  for (long long v0 = static_cast<long long>(blockIdx.x) * 32; v0 < p.vocab; v0 += static_cast<long long>(gridDim.x) * 32) {
+    const bool none = v0 + lane < p.vocab && p.first[v0 + lane] == 0;
+    if (bytes % 16 == 0) {
+      if (none) {
+        char* out = static_cast<char*>(p.grad) + (v0 + lane) * bytes;
+        for (long long at = 0; at < bytes; at += kZeroBytes)
+          sm100::bulk_store(out + at, zeros, static_cast<uint32_t>(min(static_cast<long long>(kZeroBytes), bytes - at)));
+        sm100::bulk_commit_group();
+      }
+    } else {
+      for (uint32_t rows = __ballot_sync(0xffffffffu, none); rows; rows &= rows - 1) {
+        G* out = static_cast<G*>(p.grad) + (v0 + __ffs(rows) - 1) * p.dim;
+        for (int c = lane; c < p.dim; c += 32) out[c] = from_f32<G>(0.f);
+      }
+    }
+  }
+  sm100::bulk_wait_group<0>();   // shared memory stays until it is read, and the zeros are written
+}
+
+// Every row that is the sum of one run or piece, and the rows without a token.
+// Eight warps of a block add: first the pieces of long runs, a block each, then
+// the short runs, a warp (or a group of its lanes) per run and row piece, while
+// the ninth writes zeros: the reads of some rows and the writes of others share
+// the memory's time.
 template <typename D, typename G, bool VEC>
-__global__ void __launch_bounds__(32 * kEmbWarps, 4) embedding_row_kernel(const EmbedGradParams p, const EmbedShape sh) {
+__global__ void __launch_bounds__(32 * (kEmbWarps + 1), 3) embedding_rows_kernel(const EmbedGradParams p, uint32_t segs,
+                                                                                 int lpr) {
+  __shared__ float part[kEmbWarps][kSumUnits * 8][32];
+  __shared__ __align__(128) uint4 zeros[kZeroBytes / 16];
+  pdl_launch_dependents();
+  if (threadIdx.y == kEmbWarps && !p.accumulate) {
+    for (int i = threadIdx.x; i < kZeroBytes / 16; i += 32) zeros[i] = make_uint4(0, 0, 0, 0);
+    sm100::fence_proxy_async_smem();
+    __syncwarp();
+  }
+  pdl_wait();
+  if (threadIdx.y == kEmbWarps) {
+    if (!p.accumulate) fill_rows<G>(p, zeros);
+    return;
+  }
+  add_long<D, G, VEC, false>(p, segs, part);
+  const uint2* sorted = p.sorted[(p.passes + 1) & 1];
+  const int l = threadIdx.x % lpr;
+  const uint32_t per_warp = 32 / lpr, count = p.counts->shorts;
+  // tasks: row pieces of groups of per_warp runs
+  const unsigned long long tasks = static_cast<unsigned long long>((count + per_warp - 1) / per_warp) * segs;
+  for (unsigned long long it = blockIdx.x * kEmbWarps + threadIdx.y; it < tasks; it += gridDim.x * kEmbWarps) {
+    const uint32_t q = it <= 0xffffffffull ? static_cast<uint32_t>(it) / segs : static_cast<uint32_t>(it / segs);
+    const int c0 = static_cast<int>(it - static_cast<unsigned long long>(q) * segs) * (32 * 8 * kSumUnits);
+    const uint32_t i = q * per_warp + threadIdx.x / lpr;
+    if (i >= count) continue;
+    const uint4 w = p.shorts[i];
+    Sums<kSumUnits> a = {};
+    add_rows<D, VEC, VEC ? 4 : 2>(
+        w.y, w.z, p.dim, c0, lpr, l, a,
+        [&](uint32_t k) { return static_cast<const D*>(p.dout) + sorted[k].y * p.dout_ld; });
+    write_row<G, VEC>(p, static_cast<G*>(p.grad) + static_cast<long long>(w.x) * p.dim, c0, lpr, l, a);
+  }
+}
+
+// Runs of several pieces.
+template <typename G, bool VEC>
+__global__ void __launch_bounds__(32 * kEmbWarps) embedding_join_kernel(const EmbedGradParams p, uint32_t segs) {
+  __shared__ float part[kEmbWarps][kSumUnits * 8][32];
   pdl_launch_dependents();
   pdl_wait();
-  const LaneRow w = lane_row(sh);
-  if (w.row >= p.vocab || w.c0 >= p.dim) return;
-  const uint32_t lo = p.lo[w.row], hi = p.hi[w.row];
-  if ((lo == hi && p.accumulate) || hi - lo > kEmbedLongRun) return;
-  const uint32_t* pos = p.pos[(p.passes + 1) & 1];
-  Sums a = {};
-  add_rows<D, VEC, VEC && sizeof(D) == 2 ? 2 : 1>(
-      lo, hi, p.dim, w.c0, sh.lpr, w.l, a,
-      [&](uint32_t i) { return static_cast<const D*>(p.dout) + pos[i] * p.dout_ld; });
-  write_row<G, VEC>(p, static_cast<G*>(p.grad) + w.row * p.dim, w.c0, sh.lpr, w.l, a);
+  add_long<float, G, VEC, true>(p, segs, part);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -545,9 +624,8 @@ cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   int limit = 8;
   if (e == cudaSuccess) e = sort_limit(&limit);
   if (e != cudaSuccess) return e;
-  const long long want = std::max((p.n + 2047) / 2048, p.vocab / 16384);
   unsigned nb = 1;
-  while (static_cast<int>(nb) < limit && nb < want) nb *= 2;
+  while (static_cast<int>(nb) < limit && nb < (p.n + 2047) / 2048) nb *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nb);
   cfg.blockDim = dim3(kSortThreads);
@@ -565,29 +643,14 @@ cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, embedding_sort_kernel, p);
 }
 
+static uint32_t sum_segments(int dim) { return (dim + 32 * 8 * kSumUnits - 1) / (32 * 8 * kSumUnits); }
+
 template <typename D, typename G, bool VEC>
 static cudaError_t rows_typed(const EmbedGradParams& p, cudaStream_t s) {
-  const EmbedLaunch l = embed_launch(p.vocab, p.dim, kSumUnits);
-  return launch_pdl(embedding_row_kernel<D, G, VEC>, l.grid, l.block, 0, s, p, l.shape);
-}
-template <typename D, typename G, bool VEC>
-static cudaError_t long_typed(const EmbedGradParams& p, bool join, cudaStream_t s) {
-  constexpr int kCols = 32 * 8 * kSumUnits;
-  const int segs = (p.dim + kCols - 1) / kCols;
-  // at most n / (kEmbedLongRun + 1) runs are long, n / (kEmbedPiece + 1) of several pieces
-  const long long most = (join ? p.n / (kEmbedPiece + 1) : embed_max_items(p.n)) * segs;
-  const dim3 grid(static_cast<unsigned>(std::min<long long>(most, 2 * p.sms)));
-  if (join) return launch_pdl(embedding_long_kernel<D, G, VEC, true>, grid, dim3(32, kEmbWarps), 0, s, p, segs);
-  return launch_pdl(embedding_long_kernel<D, G, VEC, false>, grid, dim3(32, kEmbWarps), 0, s, p, segs);
-}
-cudaError_t launch_embedding_long(const EmbedGradParams& p, bool join, cudaStream_t s) {
-  using F = cudaError_t (*)(const EmbedGradParams&, bool, cudaStream_t);
-  using B = __nv_bfloat16;
-  static const F table[2][2][2] = {
-      {{long_typed<float, float, false>, long_typed<float, float, true>},
-       {long_typed<float, B, false>, long_typed<float, B, true>}},
-      {{long_typed<B, float, false>, long_typed<B, float, true>}, {long_typed<B, B, false>, long_typed<B, B, true>}}};
-  return table[p.dout_bf16][p.grad_bf16][p.vec](p, join, s);
+  int lpr = 32;
+  while (lpr > 1 && p.dim <= lpr / 2 * 8 * kSumUnits) lpr /= 2;
+  return launch_pdl(embedding_rows_kernel<D, G, VEC>, dim3(3 * p.sms), dim3(32, kEmbWarps + 1), 0, s, p,
+                    sum_segments(p.dim), lpr);
 }
 cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s) {
   using F = cudaError_t (*)(const EmbedGradParams&, cudaStream_t);
@@ -597,6 +660,19 @@ cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s) {
        {rows_typed<float, B, false>, rows_typed<float, B, true>}},
       {{rows_typed<B, float, false>, rows_typed<B, float, true>}, {rows_typed<B, B, false>, rows_typed<B, B, true>}}};
   return table[p.dout_bf16][p.grad_bf16][p.vec](p, s);
+}
+
+template <typename G, bool VEC>
+static cudaError_t join_typed(const EmbedGradParams& p, cudaStream_t s) {
+  const uint32_t segs = sum_segments(p.dim);
+  const long long most = p.n / (kEmbedPiece + 1) * segs;   // runs of several pieces
+  return launch_pdl(embedding_join_kernel<G, VEC>, dim3(static_cast<unsigned>(std::min<long long>(most, 3 * p.sms))),
+                    dim3(32, kEmbWarps), 0, s, p, segs);
+}
+cudaError_t launch_embedding_join(const EmbedGradParams& p, cudaStream_t s) {
+  using B = __nv_bfloat16;
+  if (p.grad_bf16) return p.vec ? join_typed<B, true>(p, s) : join_typed<B, false>(p, s);
+  return p.vec ? join_typed<float, true>(p, s) : join_typed<float, false>(p, s);
 }
 
 }  // namespace muon

@@ -119,8 +119,8 @@ def test_workspace_sizes_refuse_and_grow(L):
     assert api.muon_embedding_grad_workspace_size(8, 0, 8) == 0
     assert api.muon_embedding_grad_workspace_size(8, 8, -1) == 0
     small, big = (api.muon_embedding_grad_workspace_size(50304, 768, n) for n in (64, 65536))
-    # two sort buffers of ids and positions, the runs, and the chunks' sums
-    assert 8 * 50304 < small < big and big >= 20 * 65536 + 65536 // 128 * 768 * 4
+    # two sort buffers of ids and positions, offsets, the runs, and the pieces' sums
+    assert 4 * 50304 < small < big and big >= 20 * 65536 + 65536 // 128 * 768 * 4
     assert api.muon_layer_norm_backward_workspace_size(8, 16385) == 0
     assert api.muon_layer_norm_backward_workspace_size(0, 64) > 0
     assert api.muon_checkpoint_weight_grad_workspace_size(8, 8, 8, torch.float16) == 0
