@@ -27,7 +27,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["muon_api.cu", "k_elementwise.cu", "k_gemm_tc.cu", "k_gemm_simt.cu", "muon_noalloc.cu",
            "grad_api.cu", "k_embedding.cu", "k_layer_norm.cu", "k_checkpoint.cu", "k_weight_grad.cu"]
-HEADERS = ["common.cuh", "elt_params.cuh", "sm100.cuh", "pdl.cuh", "host_api.cuh", "grad_params.cuh", "vec8.cuh"]
+HEADERS = ["common.cuh", "elt_params.cuh", "sm100.cuh", "pdl.cuh", "host_api.cuh", "grad_params.cuh", "vec8.cuh",
+           "e4m3.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
           "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

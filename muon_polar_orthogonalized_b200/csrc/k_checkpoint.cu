@@ -17,14 +17,19 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "e4m3.cuh"
 #include "grad_params.cuh"
 #include "pdl.cuh"
 #include "vec8.cuh"
 
 namespace muon {
 
-constexpr int kCkThreads = 256;
-constexpr int kCkWarps = kCkThreads / 32;
+// Launch shape: blocks of eight warps, `wx` side by side along a row and 8 / wx
+// rows apart.  A lane takes 16 adjacent features at a time (8 lanes share an
+// exponent), kCkUnits times, 512 apart; no index is divided.
+constexpr int kCkWarps = 8;
+constexpr int kCkUnits = 2;
+constexpr int kCkCols = 512 * kCkUnits;   // of a warp
 constexpr int kNanExp = 255;
 
 __device__ __forceinline__ float exp2i(int p) {   // 2^p, -126 <= p <= 127
@@ -42,93 +47,173 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
   return (p < -124 ? -124 : p) + 127;
 }
 
-// A warp packs 256 columns of a row: lane l the 8 columns from 8 l, so that
-// 16 lanes share a block.
+// 16 features from column c on; zeros past the row.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kCkThreads) checkpoint_pack_kernel(const CkptParams p, int nseg) {
+struct Feat16 {
+  Raw8<T> r[2];
+  __device__ __forceinline__ void load(const T* row, int c, int cols) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      r[h] = Raw8<T>{};
+      if constexpr (VEC) {
+        if (c + 8 * h < cols) r[h] = load_raw8(row + c + 8 * h);
+      } else {
+        T* e = reinterpret_cast<T*>(&r[h]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + 8 * h + k < cols) e[k] = row[c + 8 * h + k];
+      }
+    }
+  }
+  // bits of the largest magnitude as fp32 (magnitudes order like their bits; NaN is the largest)
+  __device__ __forceinline__ uint32_t amax() const {
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {r[h].w[0].x, r[h].w[0].y, r[h].w[0].z, r[h].w[0].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t a = w[k] & 0x7fff7fffu;
+          m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&a));
+        }
+      }
+      const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+      return max(b << 16, b & 0xffff0000u);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+        unpack8(r[h], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+      }
+      return m;
+    }
+  }
+  // codes of the values times f, a power of two.  In bf16 the product is exact
+  // but where it falls below 2^-126, far under half the smallest code.
+  __device__ __forceinline__ uint4 codes(float f) const {
+    uint32_t out[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+      if constexpr (sizeof(T) == 2) {
+        const __nv_bfloat162 ff = __float2bfloat162_rn(f);
+        uint4 w = r[h].w[0];
+        uint32_t* q = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&q[k]), ff);
+          q[k] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        Raw8<T> s;
+        s.w[0] = w;
+        unpack8(s, v);
+      } else {
+        unpack8(r[h], v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= f;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t a =
+            __nv_cvt_float2_to_fp8x2(make_float2(v[4 * q], v[4 * q + 1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t b =
+            __nv_cvt_float2_to_fp8x2(make_float2(v[4 * q + 2], v[4 * q + 3]), __NV_SATFINITE, __NV_E4M3);
+        out[2 * h + q] = a | (b << 16);
+      }
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+  }
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kCkWarps) checkpoint_pack_kernel(const CkptParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long task = static_cast<long long>(blockIdx.x) * kCkWarps + (threadIdx.x >> 5);
-  const long long row = task / nseg;
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
   if (row >= p.rows) return;
-  const int lane = threadIdx.x & 31;
-  const int c = static_cast<int>(task - row * nseg) * 256 + lane * 8;
+  const int c0 = (blockIdx.y * blockDim.y + threadIdx.y) * kCkCols + threadIdx.x * 16;
   const T* x = static_cast<const T*>(p.x) + row * p.x_ld;
-  float v[8] = {};
-  if constexpr (VEC) {
-    if (c < p.cols) load8(x + c, v);
-  } else {
+  Feat16<T, VEC> v[kCkUnits];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < p.cols) v[k] = to_f32(x[c + k]);
+  for (int u = 0; u < kCkUnits; ++u) v[u].load(x, c0 + 512 * u, p.cols);
+#pragma unroll
+  for (int u = 0; u < kCkUnits; ++u) {
+    const int c = c0 + 512 * u;
+    uint32_t amax = v[u].amax();
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int e = block_exponent(amax);
+    if (c < p.q_ld)
+      *reinterpret_cast<uint4*>(p.q + row * p.q_ld + c) = v[u].codes(e == kNanExp ? 0.f : exp2i(127 - e));
+    if ((threadIdx.x & 7) == 0 && c < p.cols) p.exps[row * p.nblk + c / kCkptBlock] = static_cast<uint8_t>(e);
   }
-  uint32_t amax = 0;   // magnitudes order like their bits; NaN is the largest
-#pragma unroll
-  for (int k = 0; k < 8; ++k) amax = max(amax, __float_as_uint(v[k]) & 0x7fffffffu);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const int e = block_exponent(amax);
-  if (c >= p.q_ld) return;
-  const float f = e == kNanExp ? 0.f : exp2i(127 - e);
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] * f, v[4 * h + 1] * f), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t b =
-        __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] * f, v[4 * h + 3] * f), __NV_SATFINITE, __NV_E4M3);
-    w[h] = a | (b << 16);
-  }
-  *reinterpret_cast<uint2*>(p.q + row * p.q_ld + c) = make_uint2(w[0], w[1]);
-  if ((lane & 15) == 0 && c < p.cols) p.exps[row * p.nblk + c / kCkptBlock] = static_cast<uint8_t>(e);
-}
-
-// 2 codes -> 2 floats, exact.
-__device__ __forceinline__ float2 codes2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-// The factor of an exponent byte; 255 gives NaN.
-__device__ __forceinline__ float block_factor(int e) {
-  return e == kNanExp ? __uint_as_float(0x7fffffffu) : exp2i(e - 127);
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kCkThreads) checkpoint_unpack_kernel(const CkptParams p, int nseg) {
+__global__ void __launch_bounds__(32 * kCkWarps) checkpoint_unpack_kernel(const CkptParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long task = static_cast<long long>(blockIdx.x) * kCkWarps + (threadIdx.x >> 5);
-  const long long row = task / nseg;
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
   if (row >= p.rows) return;
-  const int lane = threadIdx.x & 31;
-  const int c = static_cast<int>(task - row * nseg) * 256 + lane * 8;
-  if (c >= p.cols) return;
-  const uint2 q = *reinterpret_cast<const uint2*>(p.q + row * p.q_ld + c);
-  const float f = block_factor(p.exps[row * p.nblk + c / kCkptBlock]);
-  float v[8];
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const float2 u = codes2(((h < 2 ? q.x : q.y) >> ((h & 1) * 16)) & 0xffffu);
-    v[2 * h] = u.x * f;
-    v[2 * h + 1] = u.y * f;
-  }
+  const int c0 = (blockIdx.y * blockDim.y + threadIdx.y) * kCkCols + threadIdx.x * 16;
   T* out = static_cast<T*>(p.out) + row * p.out_ld;
-  if constexpr (VEC) {
-    store8(out + c, v);
-  } else {
+  uint4 q[kCkUnits];
+  int e[kCkUnits];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < p.cols) out[c + k] = from_f32<T>(v[k]);
+  for (int u = 0; u < kCkUnits; ++u) {
+    const int c = c0 + 512 * u;
+    if (c >= p.cols) break;
+    q[u] = *reinterpret_cast<const uint4*>(p.q + row * p.q_ld + c);
+    e[u] = p.exps[row * p.nblk + c / kCkptBlock];
+  }
+#pragma unroll
+  for (int u = 0; u < kCkUnits; ++u) {
+    const int c = c0 + 512 * u;
+    if (c >= p.cols) break;
+    uint4 r[2];
+    restore16(q[u], e[u], r[0], r[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // features 1 and 2 of every four back in place
+      Raw8<__nv_bfloat16> b;
+      b.w[0] = make_uint4(__byte_perm(r[h].x, r[h].y, 0x5410), __byte_perm(r[h].x, r[h].y, 0x7632),
+                          __byte_perm(r[h].z, r[h].w, 0x5410), __byte_perm(r[h].z, r[h].w, 0x7632));
+      const int cc = c + 8 * h;
+      if constexpr (VEC && sizeof(T) == 2) {
+        if (cc < p.cols) *reinterpret_cast<uint4*>(out + cc) = b.w[0];
+      } else {
+        float v[8];
+        unpack8(b, v);
+        if constexpr (VEC) {
+          if (cc < p.cols) store8(out + cc, v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (cc + k < p.cols) out[cc + k] = from_f32<T>(v[k]);
+        }
+      }
+    }
   }
 }
 
 // ---------------------------------------------------------------- launchers
-static int ck_segments(long long cols) { return static_cast<int>((cols + 255) / 256); }
-static dim3 ck_grid(long long tasks) { return dim3(static_cast<unsigned>((tasks + kCkWarps - 1) / kCkWarps)); }
+static void ck_shape(long long rows, long long cols, dim3& grid, dim3& block) {
+  const unsigned segs = static_cast<unsigned>((cols + kCkCols - 1) / kCkCols);
+  unsigned wx = 1;
+  while (wx < kCkWarps && wx < segs) wx *= 2;
+  block = dim3(32, wx, kCkWarps / wx);
+  grid = dim3(static_cast<unsigned>((rows + block.z - 1) / block.z), (segs + wx - 1) / wx);
+}
 
 template <typename T, bool VEC>
 static cudaError_t pack_typed(const CkptParams& p, cudaStream_t s) {
-  const int nseg = ck_segments(p.q_ld);
-  return launch_pdl(checkpoint_pack_kernel<T, VEC>, ck_grid(p.rows * nseg), dim3(kCkThreads), 0, s, p, nseg);
+  dim3 grid, block;
+  ck_shape(p.rows, p.q_ld, grid, block);
+  return launch_pdl(checkpoint_pack_kernel<T, VEC>, grid, block, 0, s, p);
 }
 cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s) {
   if (p.bf16) return p.vec ? pack_typed<__nv_bfloat16, true>(p, s) : pack_typed<__nv_bfloat16, false>(p, s);
@@ -136,8 +221,9 @@ cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s) {
 }
 template <typename T, bool VEC>
 static cudaError_t unpack_typed(const CkptParams& p, cudaStream_t s) {
-  const int nseg = ck_segments(p.cols);
-  return launch_pdl(checkpoint_unpack_kernel<T, VEC>, ck_grid(p.rows * nseg), dim3(kCkThreads), 0, s, p, nseg);
+  dim3 grid, block;
+  ck_shape(p.rows, p.cols, grid, block);
+  return launch_pdl(checkpoint_unpack_kernel<T, VEC>, grid, block, 0, s, p);
 }
 cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s) {
   if (p.bf16) return p.vec ? unpack_typed<__nv_bfloat16, true>(p, s) : unpack_typed<__nv_bfloat16, false>(p, s);

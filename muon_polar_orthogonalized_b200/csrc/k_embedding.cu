@@ -144,6 +144,9 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t act, uint32_t d) {
 // of the 32, and the first of them adds their number to the count in shared
 // memory.  Placing, a key goes to the start of its digit, plus what earlier
 // blocks and warps hold of it, plus its offset.
+// ONE: a lane's keys are at most kSortKeys, and stay in its registers between
+// counting and placing; else they and their offsets are read again.
+template <bool ONE>
 __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const EmbedGradParams p) {
   extern __shared__ __align__(128) uint32_t sm[];
   uint32_t* hist = sm;                                  // [warp][bin]
@@ -192,8 +195,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
 #pragma unroll
     for (int b = 0; b < kSortBins; b += 128) *reinterpret_cast<uint4*>(mine + b + lane * 4) = make_uint4(0, 0, 0, 0);
     __syncwarp();
+    uint2 key[kSortKeys];
+    uint32_t off[kSortKeys];
     for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortKeys) {
-      uint2 key[kSortKeys];
       load_keys(i0, key);
 #pragma unroll
       for (int k = 0; k < kSortKeys; ++k) {
@@ -204,7 +208,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
           const uint32_t d = (key[k].x >> shift) & (kSortBins - 1);
           const uint32_t peers = same_digit(act, d);
           const uint32_t rk = __popc(peers & ((1u << lane) - 1)), so_far = mine[d];
-          p.offset[i] = so_far + rk;
+          off[k] = so_far + rk;
+          if (!ONE) p.offset[i] = off[k];
           __syncwarp(act);
           if (rk == 0) mine[d] = so_far + __popc(peers);
         }
@@ -255,13 +260,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
     }
     __syncthreads();
     for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortKeys) {
-      uint2 key[kSortKeys];
-      uint32_t off[kSortKeys];
-      load_keys(i0, key);
+      if (!ONE) {
+        load_keys(i0, key);
 #pragma unroll
-      for (int k = 0; k < kSortKeys; ++k) {
-        const uint32_t i = i0 + k * 32 + lane;
-        off[k] = i < end ? p.offset[i] : 0;
+        for (int k = 0; k < kSortKeys; ++k) {
+          const uint32_t i = i0 + k * 32 + lane;
+          off[k] = i < end ? p.offset[i] : 0;
+        }
       }
 #pragma unroll
       for (int k = 0; k < kSortKeys; ++k) {
@@ -592,9 +597,9 @@ cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s) {
   return table[p.table_bf16][p.out_bf16][p.vec](p, s);
 }
 
-// Blocks of the sort's cluster: enough that a lane has few keys, and that
-// clearing the runs of a large table is shared.  16 where the GPU can place
-// such a cluster (beyond the portable 8).
+// Blocks of the sort's cluster: enough that a lane has few keys.  16 where the
+// GPU can place such a cluster (beyond the portable 8).
+template <bool ONE>
 static cudaError_t sort_limit(int* limit) {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -613,19 +618,23 @@ static cudaError_t sort_limit(int* limit) {
   cfg.numAttrs = 1;
   int clusters = 0;
   *limit = 8;
-  if (cudaOccupancyMaxActiveClusters(&clusters, embedding_sort_kernel, &cfg) == cudaSuccess && clusters > 0) *limit = 16;
+  if (cudaOccupancyMaxActiveClusters(&clusters, embedding_sort_kernel<ONE>, &cfg) == cudaSuccess && clusters > 0) *limit = 16;
   else cudaGetLastError();
   if (dev < 64) known[dev].store(*limit, std::memory_order_relaxed);
   return cudaSuccess;
 }
-cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+template <bool ONE>
+static cudaError_t sort_launch(const EmbedGradParams& p, unsigned nb, cudaStream_t s) {
+  auto kern = embedding_sort_kernel<ONE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   int limit = 8;
-  if (e == cudaSuccess) e = sort_limit(&limit);
+  if (e == cudaSuccess) e = sort_limit<ONE>(&limit);
   if (e != cudaSuccess) return e;
-  unsigned nb = 1;
-  while (static_cast<int>(nb) < limit && nb < (p.n + 2047) / 2048) nb *= 2;
+  if (nb > static_cast<unsigned>(limit)) {
+    nb = limit;
+    if (ONE && p.n > static_cast<long long>(nb) * kSortThreads * kSortKeys) return sort_launch<false>(p, nb, s);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nb);
   cfg.blockDim = dim3(kSortThreads);
@@ -640,7 +649,14 @@ cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, embedding_sort_kernel, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
+  unsigned nb = 1;
+  while (nb < 16 && nb < std::max((p.n + 2047) / 2048, p.vocab / 65536)) nb *= 2;
+  // per warp, positions are rounded up to 32
+  const bool one = p.n <= static_cast<long long>(nb) * kSortThreads * kSortKeys;
+  return one ? sort_launch<true>(p, nb, s) : sort_launch<false>(p, nb, s);
 }
 
 static uint32_t sum_segments(int dim) { return (dim + 32 * 8 * kSumUnits - 1) / (32 * 8 * kSumUnits); }
