@@ -206,6 +206,7 @@ static void ck_shape(long long rows, long long cols, dim3& grid, dim3& block) {
   unsigned wx = 1;
   while (wx < kCkWarps && wx < segs) wx *= 2;
   block = dim3(32, wx, kCkWarps / wx);
+  while (block.z > 1 && rows * segs < 8 * 148 * block.z) block.z /= 2;   // few rows: spread over the SMs
   grid = dim3(static_cast<unsigned>((rows + block.z - 1) / block.z), (segs + wx - 1) / wx);
 }
 

@@ -418,9 +418,9 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormP
   }
 }
 
-// dgain / dbias (+)= the blocks' partial rows, added in a fixed tree: 16
-// threads per column take every 16th row each, then their sums are added.
-constexpr int kColThreads = 16;
+// dgain / dbias (+)= the blocks' partial rows, added in a fixed tree: 32
+// threads per column take every 32nd row each, then their sums are added.
+constexpr int kColThreads = 32;
 template <typename G>
 __global__ void __launch_bounds__(32 * kColThreads) layer_norm_column_kernel(const NormParams p) {
   __shared__ float part[kColThreads][33];
