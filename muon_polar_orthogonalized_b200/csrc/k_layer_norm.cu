@@ -36,21 +36,39 @@ namespace muon {
 constexpr int kNormThreads = 256;   // of a block that holds several groups
 
 // Where a row's columns live: blockDim.x threads (a multiple of 32) per group,
-// blockDim.y groups.  Unit i of thread t is 8 adjacent columns (VEC) or 8 that
-// lie blockDim.x apart.
-template <bool VEC>
+// blockDim.y groups.  Unit i of thread t is 8 columns: adjacent ones (bf16 rows),
+// two runs of 4 (fp32 rows, so that neighbouring threads' 16-byte accesses adjoin
+// there too: with 8 adjacent ones every sector is fetched twice), or, without
+// VEC, 8 that lie blockDim.x apart.
+template <bool VEC, bool SPLIT>
 struct Cols {
   static __device__ __forceinline__ int at(int i, int e) {
     const int t = threadIdx.x, n = blockDim.x;
-    return VEC ? (i * n + t) * 8 + e : (i * 8 + e) * n + t;
+    if (!VEC) return (i * 8 + e) * n + t;
+    return SPLIT ? ((2 * i + e / 4) * n + t) * 4 + e % 4 : (i * n + t) * 8 + e;
   }
-  // whether a unit holds any of the row's columns (VEC: then all 8)
+  // whether a unit holds any of the row's columns
   static __device__ __forceinline__ bool inside(int i, int cols) { return at(i, 0) < cols; }
-  // units that are inside only; scalar columns past the row load as zeros
+  // units that are inside only; columns past the row load as zeros
   template <typename T>
   static __device__ __forceinline__ void load(const T* row, int i, int cols, float2 (&v)[4]) {
-    if constexpr (VEC) {
+    if constexpr (VEC && !SPLIT) {
       unpack4x2(load_raw8(row + at(i, 0)), v);
+    } else if constexpr (VEC) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const T* q = row + at(i, 4 * h);
+        const bool in = at(i, 4 * h) < cols;
+        if constexpr (sizeof(T) == 4) {
+          const float4 f = in ? *reinterpret_cast<const float4*>(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[2 * h] = make_float2(f.x, f.y);
+          v[2 * h + 1] = make_float2(f.z, f.w);
+        } else {
+          const uint2 w = in ? *reinterpret_cast<const uint2*>(q) : make_uint2(0, 0);
+          v[2 * h] = make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+          v[2 * h + 1] = make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        }
+      }
     } else {
       float f[8];
 #pragma unroll
@@ -62,17 +80,33 @@ struct Cols {
   template <typename T>
   static __device__ __forceinline__ void store(T* row, int i, int cols, const float2 (&v)[4]) {
     const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-    if constexpr (VEC) {
+    if constexpr (VEC && !SPLIT) {
       store8(row + at(i, 0), f);
+    } else if constexpr (VEC) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        T* q = row + at(i, 4 * h);
+        if (at(i, 4 * h) >= cols) continue;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(q) = make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+        } else {
+          const __nv_bfloat162 a = __floats2bfloat162_rn(f[4 * h], f[4 * h + 1]);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(f[4 * h + 2], f[4 * h + 3]);
+          *reinterpret_cast<uint2*>(q) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        }
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (at(i, e) < cols) row[at(i, e)] = from_f32<T>(f[e]);
     }
   }
-  // zeros in the scalar columns past the row (VEC: there are none)
+  // zeros in an inside unit's columns past the row
   static __device__ __forceinline__ void trim(int i, int cols, float2 (&v)[4]) {
-    if constexpr (!VEC) {
+    if constexpr (VEC && SPLIT) {
+      if (at(i, 4) >= cols) v[2] = v[3] = make_float2(0.f, 0.f);
+    } else if constexpr (!VEC) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (at(i, 2 * k) >= cols) v[k].x = 0.f;
@@ -94,14 +128,20 @@ struct Ring {
   __device__ __forceinline__ uint4* slot(int stage, int piece) const {
     return slots + (stage * PER + piece) * threads + tid;
   }
-  // 8 elements (sizeof(T) / 2 pieces from `piece` on) of one unit
-  template <typename T>
-  __device__ __forceinline__ void copy(int stage, int piece, const T* src) const {
+  // zeros in every slot: the pieces past the row are never copied to
+  __device__ __forceinline__ void clear() const {
 #pragma unroll
-    for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) {
+    for (int k = 0; k < K * PER; ++k) slots[k * threads + tid] = make_uint4(0, 0, 0, 0);
+  }
+  // unit i of a row, in sizeof(T) / 2 pieces from `piece` on
+  template <typename C, typename T>
+  __device__ __forceinline__ void copy(int stage, int piece, const T* row, int i, int cols) const {
+    constexpr int H = static_cast<int>(sizeof(T) / 2);
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      const int c = C::at(i, h * 8 / H);
       const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot(stage, piece + h)));
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<const uint4*>(src) + h)
-                   : "memory");
+      if (c < cols) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row + c) : "memory");
     }
   }
   template <typename T>
@@ -169,13 +209,14 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) 
 // and bias stay in registers.
 template <typename X, typename Y, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
 __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const NormParams p) {
-  using C = Cols<VEC>;
+  using C = Cols<VEC, sizeof(X) == 4>;
   constexpr int UP = static_cast<int>(sizeof(X)) / 2;   // 16-byte pieces per unit
   extern __shared__ uint4 ring_smem[];
   __shared__ float red[2 * R * 32];
   const Ring<K, R * UNITS * UP> ring(ring_smem);
   int flip = 0;
   pdl_launch_dependents();
+  if (VEC) ring.clear();
   pdl_wait();
   const float n = static_cast<float>(p.cols);
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y * R;
@@ -188,7 +229,7 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const NormParams
         const X* x = static_cast<const X*>(p.x) + (first + r) * p.x_ld;
 #pragma unroll
         for (int i = 0; i < UNITS; ++i)
-          if (C::inside(i, p.cols)) ring.copy(stage, (r * UNITS + i) * UP, x + C::at(i, 0));
+          ring.template copy<C>(stage, (r * UNITS + i) * UP, x, i, p.cols);
       }
     }
     ring.commit();
@@ -280,7 +321,7 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const NormParams
 // --------------------------------------------------------------- backward
 template <typename X, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
 __global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormParams p) {
-  using C = Cols<VEC>;
+  using C = Cols<VEC, sizeof(X) == 4>;
   constexpr int UP = static_cast<int>(sizeof(X)) / 2;
   extern __shared__ uint4 ring_smem[];
   __shared__ float red[2 * 2 * R * 32];
@@ -288,6 +329,7 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormP
   int flip = 0;
   float2 dg[UNITS][4] = {}, db[UNITS][4] = {}, g[UNITS][4] = {};
   pdl_launch_dependents();
+  if (VEC) ring.clear();
   pdl_wait();
   const float n = static_cast<float>(p.cols);
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y * R;
@@ -300,11 +342,10 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormP
         const X* x = static_cast<const X*>(p.x) + (first + r) * p.x_ld;
         const X* dy = static_cast<const X*>(p.dy) + (first + r) * p.dy_ld;
 #pragma unroll
-        for (int i = 0; i < UNITS; ++i)
-          if (C::inside(i, p.cols)) {
-            ring.copy(stage, (r * UNITS + i) * 2 * UP, x + C::at(i, 0));
-            ring.copy(stage, (r * UNITS + i) * 2 * UP + UP, dy + C::at(i, 0));
-          }
+        for (int i = 0; i < UNITS; ++i) {
+          ring.template copy<C>(stage, (r * UNITS + i) * 2 * UP, x, i, p.cols);
+          ring.template copy<C>(stage, (r * UNITS + i) * 2 * UP + UP, dy, i, p.cols);
+        }
       }
     }
     ring.commit();
@@ -481,7 +522,7 @@ static cudaError_t forward_shape(const NormParams& p, cudaStream_t s) {
   constexpr bool B16 = sizeof(X) == 2;
   if (p.cols <= 2048)
     return few ? forward_launch<X, Y, VEC, 1, kNormThreads, 4, 1, 2, true>(p, s)
-               : forward_launch<X, Y, VEC, 1, kNormThreads, 4, 4, 2, true>(p, s);
+               : forward_launch<X, Y, VEC, 1, kNormThreads, B16 ? 4 : 3, 4, 2, true>(p, s);
   if (p.cols <= 4096)
     return few ? forward_launch<X, Y, VEC, 2, kNormThreads, 3, 1, 2, true>(p, s)
                : forward_launch<X, Y, VEC, 2, kNormThreads, 3, B16 ? 4 : 2, 2, true>(p, s);
@@ -504,7 +545,7 @@ struct GradClass {
   int units, max_threads, per_sm;
 };
 static GradClass grad_class(int cols) {
-  if (cols <= 2048) return {1, kNormThreads, 3};
+  if (cols <= 2048) return {1, kNormThreads, 2};
   if (cols <= 4096) return {2, kNormThreads, 2};
   if (cols <= 8192) return {2, 512, 1};
   return {2, 1024, 1};
@@ -513,9 +554,7 @@ int layer_norm_grad_blocks(long long rows, int cols, int sms) {
   const GradClass c = grad_class(cols);
   const dim3 block = norm_block(c.units, cols);
   const long long per_sm = static_cast<long long>(c.per_sm) * (c.max_threads / (block.x * block.y));
-  // few rows: two blocks per SM at most, so that few partial rows are left to add
-  const long long want = (rows + block.y - 1) / block.y;
-  const long long cap = sms * (want < 8 * sms && per_sm > 2 ? 2 : per_sm);
+  const long long want = (rows + block.y - 1) / block.y, cap = sms * per_sm;
   return static_cast<int>(want < cap ? want : cap);
 }
 template <typename X, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
@@ -535,8 +574,8 @@ static cudaError_t backward_shape(const NormParams& p, cudaStream_t s) {
   constexpr bool B16 = sizeof(X) == 2;
   const bool few = p.rows <= 8ll * p.sms;   // one row at a time
   if (p.cols <= 2048)
-    return few ? backward_launch<X, VEC, 1, kNormThreads, 3, 1, 4, true>(p, s)
-               : backward_launch<X, VEC, 1, kNormThreads, 3, 2, 2, true>(p, s);
+    return few ? backward_launch<X, VEC, 1, kNormThreads, 2, 1, 4, true>(p, s)
+               : backward_launch<X, VEC, 1, kNormThreads, 2, B16 ? 4 : 2, B16 ? 2 : 3, true>(p, s);
   if (p.cols <= 4096) return backward_launch<X, VEC, 2, kNormThreads, 2, B16 ? 2 : 1, 2, true>(p, s);
   if (p.cols <= 8192) return backward_launch<X, VEC, 2, 512, 1, B16 ? 2 : 1, 2, true>(p, s);
   return backward_launch<X, VEC, 2, 1024, 1, 1, B16 ? 3 : 1, false>(p, s);
