@@ -172,12 +172,6 @@ __device__ __forceinline__ void transpose_pieces(float (&v)[4][8], int lane) {
   }
 }
 
-// 8 sums as one whole 32-byte sector (dst 32-byte aligned).
-__device__ __forceinline__ void store_sector(float* dst, const float (&v)[8]) {
-  sm100::st_global_v8(dst, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])),
-                      make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
-}
-
 // 8 columns of one row; vec: 16-byte accesses allowed and cols >= 8.
 template <typename G>
 __device__ __forceinline__ void store_piece(G* dst, float (&v)[8], int cols, bool accumulate, bool vec) {
@@ -187,12 +181,6 @@ __device__ __forceinline__ void store_piece(G* dst, float (&v)[8], int cols, boo
       load8(dst, o);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] += o[k];
-    }
-    if constexpr (sizeof(G) == 4) {
-      if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
-        store_sector(dst, v);
-        return;
-      }
     }
     store8(dst, v);
   } else {
@@ -473,7 +461,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
           const int row = row0 + i;
           if (row >= p.n) continue;
           if (u.slot >= 0)
-            store_sector(p.partial + (static_cast<long long>(u.slot) * C::TN + (row - u.n0)) * C::TK + (c0 - u.k0), v[i]);
+            store8(p.partial + (static_cast<long long>(u.slot) * C::TN + (row - u.n0)) * C::TK + (c0 - u.k0), v[i]);
           else
             store_piece(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + c0, v[i], p.k - c0,
                         p.accumulate != 0, vec && c0 + 8 <= p.k);
