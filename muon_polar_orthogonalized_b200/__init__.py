@@ -10,7 +10,7 @@ from ._native import (MUON_BF16, MUON_CAUTIOUS_WD, MUON_F32, MUON_FP32_DEBUG,  #
                       MUON_NESTEROV, MUON_NORMUON, MUON_ROW_EQUILIBRATE, MUON_TC_NARROW_TILES,
                       MUON_TC_SINGLE_CTA, MUON_TC_WIDE_TILES, MUON_UNFUSED_UPDATE, MuonError,
                       MuonGroup)
-from .api import (AdamWSpec, Checkpoint, adamw_query_status, adamw_step, adamw_step_scheduled,  # noqa: F401
+from .api import (AdamWSpec, Checkpoint, EmbeddingGrad, LinearGrad, adamw_query_status, adamw_step, adamw_step_scheduled,  # noqa: F401
                   muon_checkpoint_pack, muon_checkpoint_unpack, muon_checkpoint_weight_grad,
                   muon_checkpoint_weight_grad_workspace_size, muon_embedding_forward, muon_embedding_grad,
                   muon_embedding_grad_workspace_size, muon_layer_norm_backward,
@@ -28,7 +28,7 @@ __all__ = [
     "muon_schedule_advance", "muon_schedule_advance_cosine", "AdamWSpec", "MuonError", "MuonGroup",
     "muon_embedding_forward", "muon_embedding_grad", "muon_embedding_grad_workspace_size",
     "muon_layer_norm_forward", "muon_layer_norm_backward", "muon_layer_norm_backward_workspace_size",
-    "Checkpoint", "new_checkpoint", "muon_checkpoint_pack", "muon_checkpoint_unpack",
+    "Checkpoint", "EmbeddingGrad", "LinearGrad", "new_checkpoint", "muon_checkpoint_pack", "muon_checkpoint_unpack",
     "muon_checkpoint_weight_grad", "muon_checkpoint_weight_grad_workspace_size",
     "muon_profiler_enable", "muon_profiler_read", "muon_profiler_reset",
 ]

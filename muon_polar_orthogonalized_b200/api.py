@@ -561,6 +561,41 @@ def muon_checkpoint_weight_grad(dy, ckpt: Checkpoint, grad, workspace, accumulat
             _dtype_code(fn, "grad", grad), 1 if accumulate else 0, workspace.data_ptr(), _workspace(fn, workspace))
 
 
+class LinearGrad:
+    """The gradient of a hidden matrix W [n, k] (y = x W^T) by its factors: dy
+    [..., n] and the checkpoint of x.  MuonAdamW.step takes it in a gradient's
+    place and forms the gradient itself."""
+
+    def __init__(self, dy, checkpoint: Checkpoint):
+        self.dy, self.checkpoint = dy, checkpoint
+
+    def workspace_size(self, grad) -> int:
+        dy = self.dy
+        es = dy.element_size()
+        aligned = dy.data_ptr() % 16 == 0 and all(st * es % 16 == 0 for st in dy.stride()[:-1])
+        return muon_checkpoint_weight_grad_workspace_size(self.checkpoint.rows, grad.shape[0], grad.shape[1], dy.dtype,
+                                                          aligned)
+
+    def write(self, grad, workspace, accumulate: bool = False, stream=None) -> None:
+        muon_checkpoint_weight_grad(self.dy, self.checkpoint, grad, workspace, accumulate=accumulate, stream=stream)
+
+
+class EmbeddingGrad:
+    """The gradient of an embedding table by its factors: dout [..., dim], the
+    token ids and the lookup's scale.  MuonAdamW.step takes it in a gradient's
+    place and forms the gradient itself."""
+
+    def __init__(self, dout, ids, scale: float = 1.0):
+        self.dout, self.ids, self.scale = dout, ids, scale
+
+    def workspace_size(self, grad) -> int:
+        return muon_embedding_grad_workspace_size(grad.shape[0], grad.shape[1], self.ids.numel())
+
+    def write(self, grad, workspace, accumulate: bool = False, stream=None) -> None:
+        muon_embedding_grad(self.dout, self.ids, grad, workspace, scale=self.scale, accumulate=accumulate,
+                            stream=stream)
+
+
 def muon_query_status(workspace, stream=None) -> int:
     ws = workspace if isinstance(workspace, int) else workspace.data_ptr()
     return int(N.lib().muon_query_status(c_void_p(ws), c_void_p(_stream_handle(stream))))

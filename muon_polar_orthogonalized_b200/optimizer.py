@@ -69,6 +69,7 @@ class MuonAdamW:
         nbytes = ws_need if workspace_bytes is None else max(int(workspace_bytes), 0)
         dev = self.muon_params[0].device if self.muon_params else torch.device("cuda")
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        self._factor_workspace: Optional[torch.Tensor] = None   # grown by the gradients formed here
 
     def _groups(self, grad_dtypes):
         """Group descriptors, one gradient dtype per shape group."""
@@ -85,6 +86,28 @@ class MuonAdamW:
             out.append(dts.pop())
         return out
 
+    def _formed(self, param: torch.Tensor, grad, stream):
+        """The gradient tensor of one parameter: `grad` itself, or, where it is
+        given by its factors (api.LinearGrad, api.EmbeddingGrad, or a list of
+        them, one per micro-batch), their sum, formed in param.grad (allocated
+        in param.grad_dtype, else fp32, where there is none)."""
+        if grad is None or isinstance(grad, torch.Tensor):
+            return grad
+        parts = list(grad) if isinstance(grad, (list, tuple)) else [grad]
+        if not parts or not all(isinstance(f, (api.LinearGrad, api.EmbeddingGrad)) for f in parts):
+            raise ValueError("a gradient is a tensor, a LinearGrad or EmbeddingGrad, or a list of these")
+        if param.grad is None:
+            param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
+                                          requires_grad=False)
+        need = max(f.workspace_size(param.grad) for f in parts)
+        if self._factor_workspace is None or self._factor_workspace.numel() < need:
+            self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
+            if stream is not None:
+                self._factor_workspace.record_stream(stream)
+        for k, f in enumerate(parts):
+            f.write(param.grad, self._factor_workspace, accumulate=k > 0, stream=stream)
+        return param.grad
+
     @torch.no_grad()
     def step(self, stream=None, replicas: Optional[Sequence[Sequence[torch.Tensor]]] = None,
              muon_grads: Optional[Sequence[torch.Tensor]] = None,
@@ -95,13 +118,17 @@ class MuonAdamW:
         memory); each receives the updated values (muon_step_replicated).
         muon_grads / adamw_grads: the gradients to use instead of each
         parameter's .grad (muon_grads[k] for the k-th Muon tensor given at
-        construction, adamw_grads[g][j] for tensor j of AdamW group g)."""
+        construction, adamw_grads[g][j] for tensor j of AdamW group g).  A
+        gradient may be given by its factors (api.LinearGrad for a hidden
+        matrix whose input was kept as an 8-bit checkpoint, api.EmbeddingGrad
+        for an embedding table, or a list of them, one per micro-batch): the
+        step then forms it in the parameter's .grad, from nothing."""
         self.step_count += 1
         if self.muon_params:
             if muon_grads is not None:
                 if len(muon_grads) != len(self.muon_params):
                     raise ValueError("muon_grads must hold one gradient per Muon parameter")
-                grads = [muon_grads[k] for k in self._order]
+                grads = [self._formed(p, muon_grads[k], stream) for p, k in zip(self.muon_params, self._order)]
             else:
                 grads = [p.grad for p in self.muon_params]
             if any(g is None for g in grads):
@@ -120,7 +147,12 @@ class MuonAdamW:
         if adamw_grads is not None and len(adamw_grads) != len(self.adamw_groups):
             raise ValueError("adamw_grads must hold one list per AdamW group")
         for gi, g in enumerate(self.adamw_groups):
-            grads = list(adamw_grads[gi]) if adamw_grads is not None else [p.grad for p in g["params"]]
+            if adamw_grads is not None:
+                if len(adamw_grads[gi]) != len(g["params"]):
+                    raise ValueError(f"adamw_grads[{gi}] must hold one gradient per parameter of its group")
+                grads = [self._formed(p, x, stream) for p, x in zip(g["params"], adamw_grads[gi])]
+            else:
+                grads = [p.grad for p in g["params"]]
             if any(x is None for x in grads):
                 raise ValueError("every AdamW parameter needs a .grad")
             specs.append(api.AdamWSpec(g["params"], grads, g["exp_avg"], g["exp_avg_sq"], g["lr"],
