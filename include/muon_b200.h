@@ -332,9 +332,10 @@ muon_status adamw_step_scheduled(const adamw_group* groups, int n_groups,
  *   Activations  x, y, dy, dx, out, dout are device matrices of fp32 or bf16
  *                rows, `pitch` elements apart (pitch >= columns; the elements
  *                between are neither read nor written), each pointer aligned
- *                to its element.  Where columns are a multiple of 8, pointers
- *                16-byte aligned and rows 16-byte multiples apart, 16-byte
- *                accesses are used; the results are the same bits.
+ *                to its element.  Where columns and pitch are multiples of 8 and
+ *                every pointer is aligned to 8 elements (16 bytes of bf16, 32
+ *                of fp32, gain and bias included), 8 elements are accessed at
+ *                a time; else one, slower.
  *   Parameters   tables, gains, biases and gradients of matrices and tables
  *                are dense and 16-byte aligned; dgain and dbias aligned to
  *                their element.

@@ -45,9 +45,9 @@ muon_status check_rows(const char* what, const void* p, int32_t dtype, int64_t r
     return api_fail(MUON_ERR_INVALID_ARG, "%s: NULL or misaligned", what);
   return MUON_OK;
 }
-// Rows that 16-byte accesses of 8 elements may use.
+// Rows that can be accessed 8 elements at a time: 16 bytes of bf16, 32 of fp32.
 bool rows_vec(const void* p, int32_t dtype, int64_t cols, int64_t ld) {
-  return cols % 8 == 0 && aligned_to(p, 16) && (ld * static_cast<int64_t>(elem(dtype))) % 16 == 0;
+  return cols % 8 == 0 && aligned_to(p, 8 * elem(dtype)) && ld % 8 == 0;
 }
 muon_status check_workspace(const void* ws, size_t have, size_t need) {
   if (need == 0) return MUON_OK;
@@ -304,7 +304,8 @@ muon_status muon_layer_norm_forward(const void* x, int32_t x_dtype, int64_t x_pi
     p.cols = static_cast<int>(cols);
     p.x_bf16 = x_dtype == MUON_BF16;
     p.y_bf16 = y_dtype == MUON_BF16;
-    p.vec = rows_vec(x, x_dtype, cols, x_pitch) && rows_vec(y, y_dtype, cols, y_pitch);
+    p.vec = rows_vec(x, x_dtype, cols, x_pitch) && rows_vec(y, y_dtype, cols, y_pitch) && aligned_to(gain, 32) &&
+            aligned_to(bias, 32);
     p.eps = eps;
     p.sms = sms;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -355,7 +356,8 @@ muon_status muon_layer_norm_backward(const void* dy, int64_t dy_pitch, const voi
     p.x_bf16 = dtype == MUON_BF16;
     p.grad_bf16 = grad_dtype == MUON_BF16;
     p.accumulate = accumulate != 0;
-    p.vec = rows_vec(x, dtype, cols, x_pitch) && rows_vec(dy, dtype, cols, dy_pitch) && rows_vec(dx, dtype, cols, dx_pitch);
+    p.vec = rows_vec(x, dtype, cols, x_pitch) && rows_vec(dy, dtype, cols, dy_pitch) &&
+            rows_vec(dx, dtype, cols, dx_pitch) && aligned_to(gain, 32);
     p.sms = std::min(sms, 160);
     p.blocks = layer_norm_grad_blocks(rows, p.cols, p.sms);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -44,7 +44,7 @@ struct EmbedGradParams {
   uint32_t* first;     // [vocab] 1 + first sorted position of each id, 0 where it does not occur
   uint32_t* offset;    // [n] a key's offset within its warp and digit
   EmbedCounts* counts;
-  uint4* shorts;       // short runs: (id, first and one past the last sorted position, -)
+  uint4* shorts;       // short runs: (id, first and one past the last sorted position, the last's token)
   uint4* items;        // pieces of long runs: (id, first and one past the last sorted position, slot or kEmbedNoSlot)
   uint4* joins;        // runs of several pieces: (id, first and one past the last slot, -)
   float* partial;      // [slot][dim] sums of the pieces of such runs

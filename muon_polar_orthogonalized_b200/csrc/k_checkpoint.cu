@@ -48,21 +48,14 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
 }
 
 // 16 features from column c on; zeros past the row.
-template <typename T, bool VEC>
+template <typename T>
 struct Feat16 {
   Raw8<T> r[2];
   __device__ __forceinline__ void load(const T* row, int c, int cols) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       r[h] = Raw8<T>{};
-      if constexpr (VEC) {
-        if (c + 8 * h < cols) r[h] = load_raw8(row + c + 8 * h);
-      } else {
-        T* e = reinterpret_cast<T*>(&r[h]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + 8 * h + k < cols) e[k] = row[c + 8 * h + k];
-      }
+      if (c + 8 * h < cols) r[h] = load_raw8(row + c + 8 * h);
     }
   }
   // bits of the largest magnitude as fp32 (magnitudes order like their bits; NaN is the largest)
@@ -129,7 +122,61 @@ struct Feat16 {
   }
 };
 
-template <typename T, bool VEC>
+// Rows that 16-byte accesses do not fit: a lane takes every 32nd feature of a
+// block of 128, so that neighbouring lanes' accesses adjoin.
+template <typename T>
+__global__ void __launch_bounds__(32 * kCkWarps) checkpoint_pack_odd_kernel(const CkptParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
+  if (row >= p.rows) return;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_ld;
+  uint8_t* q = p.q + row * p.q_ld;
+  const int c0 = (blockIdx.y * blockDim.y + threadIdx.y) * kCkCols;
+  for (int b = c0; b < min(static_cast<int>(p.q_ld), c0 + kCkCols); b += kCkptBlock) {
+    float v[4];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = b + k * 32 + threadIdx.x;
+      v[k] = c < p.cols ? to_f32(x[c]) : 0.f;
+      amax = max(amax, __float_as_uint(v[k]) & 0x7fffffffu);
+    }
+    const int e = block_exponent(__reduce_max_sync(0xffffffffu, amax));
+    const float f = e == kNanExp ? 0.f : exp2i(127 - e);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = b + k * 32 + threadIdx.x;
+      if (c < p.q_ld) q[c] = __nv_cvt_float_to_fp8(v[k] * f, __NV_SATFINITE, __NV_E4M3);
+    }
+    if (threadIdx.x == 0 && b < p.cols) p.exps[row * p.nblk + b / kCkptBlock] = static_cast<uint8_t>(e);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kCkWarps) checkpoint_unpack_odd_kernel(const CkptParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
+  if (row >= p.rows) return;
+  T* out = static_cast<T*>(p.out) + row * p.out_ld;
+  const uint8_t* q = p.q + row * p.q_ld;
+  const int c0 = (blockIdx.y * blockDim.y + threadIdx.y) * kCkCols;
+  for (int b = c0; b < min(p.cols, c0 + kCkCols); b += kCkptBlock) {
+    const int e = p.exps[row * p.nblk + b / kCkptBlock];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = b + k * 32 + threadIdx.x;
+      if (c < p.cols) {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw(q[c], __NV_E4M3);
+        const float f = e == kNanExp ? __uint_as_float(0x7fffffffu) : exp2i(e - 127);
+        out[c] = from_f32<T>(__half2float(*reinterpret_cast<const __half*>(&h)) * f);
+      }
+    }
+  }
+}
+
+template <typename T>
 __global__ void __launch_bounds__(32 * kCkWarps) checkpoint_pack_kernel(const CkptParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -137,7 +184,7 @@ __global__ void __launch_bounds__(32 * kCkWarps) checkpoint_pack_kernel(const Ck
   if (row >= p.rows) return;
   const int c0 = (blockIdx.y * blockDim.y + threadIdx.y) * kCkCols + threadIdx.x * 16;
   const T* x = static_cast<const T*>(p.x) + row * p.x_ld;
-  Feat16<T, VEC> v[kCkUnits];
+  Feat16<T> v[kCkUnits];
 #pragma unroll
   for (int u = 0; u < kCkUnits; ++u) v[u].load(x, c0 + 512 * u, p.cols);
 #pragma unroll
@@ -153,7 +200,7 @@ __global__ void __launch_bounds__(32 * kCkWarps) checkpoint_pack_kernel(const Ck
   }
 }
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(32 * kCkWarps) checkpoint_unpack_kernel(const CkptParams p) {
   pdl_launch_dependents();
   pdl_wait();
@@ -183,18 +230,13 @@ __global__ void __launch_bounds__(32 * kCkWarps) checkpoint_unpack_kernel(const 
       b.w[0] = make_uint4(__byte_perm(r[h].x, r[h].y, 0x5410), __byte_perm(r[h].x, r[h].y, 0x7632),
                           __byte_perm(r[h].z, r[h].w, 0x5410), __byte_perm(r[h].z, r[h].w, 0x7632));
       const int cc = c + 8 * h;
-      if constexpr (VEC && sizeof(T) == 2) {
-        if (cc < p.cols) *reinterpret_cast<uint4*>(out + cc) = b.w[0];
+      if (cc >= p.cols) break;
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(out + cc) = b.w[0];
       } else {
         float v[8];
         unpack8(b, v);
-        if constexpr (VEC) {
-          if (cc < p.cols) store8(out + cc, v);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (cc + k < p.cols) out[cc + k] = from_f32<T>(v[k]);
-        }
+        store8(out + cc, v);
       }
     }
   }
@@ -210,25 +252,23 @@ static void ck_shape(long long rows, long long cols, dim3& grid, dim3& block) {
   grid = dim3(static_cast<unsigned>((rows + block.z - 1) / block.z), (segs + wx - 1) / wx);
 }
 
-template <typename T, bool VEC>
+template <typename T>
 static cudaError_t pack_typed(const CkptParams& p, cudaStream_t s) {
   dim3 grid, block;
   ck_shape(p.rows, p.q_ld, grid, block);
-  return launch_pdl(checkpoint_pack_kernel<T, VEC>, grid, block, 0, s, p);
+  return launch_pdl(p.vec ? checkpoint_pack_kernel<T> : checkpoint_pack_odd_kernel<T>, grid, block, 0, s, p);
 }
 cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s) {
-  if (p.bf16) return p.vec ? pack_typed<__nv_bfloat16, true>(p, s) : pack_typed<__nv_bfloat16, false>(p, s);
-  return p.vec ? pack_typed<float, true>(p, s) : pack_typed<float, false>(p, s);
+  return p.bf16 ? pack_typed<__nv_bfloat16>(p, s) : pack_typed<float>(p, s);
 }
-template <typename T, bool VEC>
+template <typename T>
 static cudaError_t unpack_typed(const CkptParams& p, cudaStream_t s) {
   dim3 grid, block;
   ck_shape(p.rows, p.cols, grid, block);
-  return launch_pdl(checkpoint_unpack_kernel<T, VEC>, grid, block, 0, s, p);
+  return launch_pdl(p.vec ? checkpoint_unpack_kernel<T> : checkpoint_unpack_odd_kernel<T>, grid, block, 0, s, p);
 }
 cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s) {
-  if (p.bf16) return p.vec ? unpack_typed<__nv_bfloat16, true>(p, s) : unpack_typed<__nv_bfloat16, false>(p, s);
-  return p.vec ? unpack_typed<float, true>(p, s) : unpack_typed<float, false>(p, s);
+  return p.bf16 ? unpack_typed<__nv_bfloat16>(p, s) : unpack_typed<float>(p, s);
 }
 
 }  // namespace muon

@@ -141,10 +141,11 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t act, uint32_t d) {
 // Enter the run [lo, hi) of sorted positions of an id.  The order of the entries
 // is no one's concern: a run's sum goes to its row, or, for long runs in pieces
 // of at most kEmbedPiece positions, to slots from which it is added in order.
+// last: the token position of the run's last entry.
 __device__ __forceinline__ void list_run(const EmbedGradParams& p, EmbedCounts& counts, uint32_t id, uint32_t lo,
-                                         uint32_t hi) {
+                                         uint32_t hi, uint32_t last) {
   if (hi - lo <= kEmbedLongRun) {
-    p.shorts[atomicAdd(&counts.shorts, 1u)] = make_uint4(id, lo, hi, 0);
+    p.shorts[atomicAdd(&counts.shorts, 1u)] = make_uint4(id, lo, hi, last);
     return;
   }
   const uint32_t pieces = (hi - lo + kEmbedPiece - 1) / kEmbedPiece;
@@ -318,11 +319,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
   }
   cluster.sync();
   for (uint32_t i0 = rank * kSortThreads + tid; i0 < n; i0 += 4 * stride) {
-    uint32_t k[4], right[4], lo[4];
+    uint32_t k[4], right[4], lo[4], at[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t i = i0 + j * stride;
-      k[j] = i < n ? sorted[i].x : vocab;
+      const uint2 e = i < n ? sorted[i] : make_uint2(vocab, 0);
+      k[j] = e.x;
+      at[j] = e.y;
       right[j] = i < n - 1 ? sorted[i + 1].x : vocab;
       if (k[j] == right[j]) k[j] = vocab;   // not a run's end
     }
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_kernel(const E
     for (int j = 0; j < 4; ++j) lo[j] = k[j] < vocab ? p.first[k[j]] - 1 : 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (k[j] < vocab) list_run(p, *p.counts, k[j], lo[j], i0 + j * stride + 1);
+      if (k[j] < vocab) list_run(p, *p.counts, k[j], lo[j], i0 + j * stride + 1, at[j]);
     }
   }
 }
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embedding_sort_small_kernel(c
       if (buf[mid].x < id) lo = mid + 1;
       else step_hi = mid;
     }
-    list_run(p, counts, id, lo, i + 1);
+    list_run(p, counts, id, lo, i + 1, key[k].y);
   }
   __syncthreads();
   if (tid == 0) {
@@ -668,19 +671,33 @@ __global__ void __launch_bounds__(32 * (kEmbWarps + 1), 3) embedding_rows_kernel
   const uint2* sorted = p.sorted[(p.passes + 1) & 1];
   const int l = threadIdx.x % lpr;
   const uint32_t per_warp = 32 / lpr, count = p.counts->shorts;
-  // tasks: row pieces of groups of per_warp runs
+  // Tasks: row pieces of groups of per_warp runs.  The next task's run is read
+  // while one is added, and a run of one token (most are) names it itself, so
+  // that only the row is waited for.
   const unsigned long long tasks = static_cast<unsigned long long>((count + per_warp - 1) / per_warp) * segs;
-  for (unsigned long long it = blockIdx.x * kEmbWarps + threadIdx.y; it < tasks; it += gridDim.x * kEmbWarps) {
+  const D* dout = static_cast<const D*>(p.dout);
+  auto task = [&](unsigned long long it, int& c0) -> uint4 {
     const uint32_t q = it <= 0xffffffffull ? static_cast<uint32_t>(it) / segs : static_cast<uint32_t>(it / segs);
-    const int c0 = static_cast<int>(it - static_cast<unsigned long long>(q) * segs) * (32 * 8 * kSumUnits);
+    c0 = static_cast<int>(it - static_cast<unsigned long long>(q) * segs) * (32 * 8 * kSumUnits);
     const uint32_t i = q * per_warp + threadIdx.x / lpr;
-    if (i >= count) continue;
-    const uint4 w = p.shorts[i];
-    Sums<kSumUnits> a = {};
-    add_rows<D, VEC, VEC ? 4 : 2>(
-        w.y, w.z, p.dim, c0, lpr, l, a,
-        [&](uint32_t k) { return static_cast<const D*>(p.dout) + sorted[k].y * p.dout_ld; });
-    write_row<G, VEC>(p, static_cast<G*>(p.grad) + static_cast<long long>(w.x) * p.dim, c0, lpr, l, a);
+    return it < tasks && i < count ? p.shorts[i] : make_uint4(0, 0, 0, 0);   // no run: nothing to do
+  };
+  int c0;
+  unsigned long long it = blockIdx.x * kEmbWarps + threadIdx.y;
+  uint4 w = task(it, c0);
+  while (it < tasks) {
+    it += gridDim.x * kEmbWarps;
+    int c0_next;
+    const uint4 w_next = task(it, c0_next);
+    if (w.z > w.y) {
+      Sums<kSumUnits> a = {};
+      add_rows<D, VEC, VEC ? 4 : 2>(w.y, w.z - 1, p.dim, c0, lpr, l, a,
+                                    [&](uint32_t k) { return dout + sorted[k].y * p.dout_ld; });
+      add_rows<D, VEC, 1>(0, 1, p.dim, c0, lpr, l, a, [&](uint32_t) { return dout + w.w * p.dout_ld; });
+      write_row<G, VEC>(p, static_cast<G*>(p.grad) + static_cast<long long>(w.x) * p.dim, c0, lpr, l, a);
+    }
+    w = w_next;
+    c0 = c0_next;
   }
 }
 

@@ -251,9 +251,21 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const NormParams
     fetch(row0 + (K - 1) * step, stage == 0 ? K - 1 : stage - 1);
     ring.wait();
     const int live = static_cast<int>(min(static_cast<long long>(R), p.rows - row0));
+    // without the ring, a short row stays in registers (R is 1)
+    constexpr bool KEEP = !VEC && R == 1;
+    float2 held[KEEP ? UNITS : 1][4];
+    if constexpr (KEEP)
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i) C::load(static_cast<const X*>(p.x) + row0 * p.x_ld, i, p.cols, held[i]);
     auto unit = [&](int r, int i, float2 (&v)[4]) {
-      if constexpr (VEC) ring.template get<X>(stage, (r * UNITS + i) * UP, v);
-      else C::load(static_cast<const X*>(p.x) + (row0 + r) * p.x_ld, i, p.cols, v);
+      if constexpr (VEC) {
+        ring.template get<X>(stage, (r * UNITS + i) * UP, v);
+      } else if constexpr (!KEEP) {
+        C::load(static_cast<const X*>(p.x) + (row0 + r) * p.x_ld, i, p.cols, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = held[i][k];
+      }
     };
     float mean[R], rstd[R];
 #pragma unroll
@@ -378,11 +390,26 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormP
     stats(row0 + step);
     ring.wait();
     const int live = static_cast<int>(min(static_cast<long long>(R), p.rows - row0));
+    // without the ring, a short row stays in registers (R is 1)
+    constexpr bool KEEP = !VEC && UNITS == 1;
+    float2 held[KEEP ? UNITS : 1][2][4];
+    if constexpr (KEEP)
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i) {
+        C::load(static_cast<const X*>(p.x) + row0 * p.x_ld, i, p.cols, held[i][0]);
+        C::load(static_cast<const X*>(p.dy) + row0 * p.dy_ld, i, p.cols, held[i][1]);
+      }
     // xh and dy of a unit that is inside, zeros past the row
     auto unit = [&](int r, int i, float2 (&xh)[4], float2 (&dy)[4]) {
       if constexpr (VEC) {
         ring.template get<X>(stage, (r * UNITS + i) * 2 * UP, xh);
         ring.template get<X>(stage, (r * UNITS + i) * 2 * UP + UP, dy);
+      } else if constexpr (KEEP) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          xh[k] = held[i][0][k];
+          dy[k] = held[i][1][k];
+        }
       } else {
         C::load(static_cast<const X*>(p.x) + (row0 + r) * p.x_ld, i, p.cols, xh);
         C::load(static_cast<const X*>(p.dy) + (row0 + r) * p.dy_ld, i, p.cols, dy);
@@ -517,6 +544,12 @@ static cudaError_t forward_launch(const NormParams& p, cudaStream_t s) {
 }
 template <typename X, typename Y, bool VEC>
 static cudaError_t forward_shape(const NormParams& p, cudaStream_t s) {
+  if constexpr (!VEC) {
+    if (p.cols <= 2048) return forward_launch<X, Y, false, 1, kNormThreads, 4, 1, 1, true>(p, s);
+    if (p.cols <= 4096) return forward_launch<X, Y, false, 2, kNormThreads, 3, 4, 1, true>(p, s);
+    if (p.cols <= 8192) return forward_launch<X, Y, false, 2, 512, 1, 4, 1, true>(p, s);
+    return forward_launch<X, Y, false, 2, 1024, 1, 2, 1, false>(p, s);
+  }
   // one row at a time while every group gets a few at most
   const bool few = p.rows <= 8ll * p.sms;
   constexpr bool B16 = sizeof(X) == 2;
@@ -571,6 +604,12 @@ static cudaError_t backward_launch(const NormParams& p, cudaStream_t s) {
 }
 template <typename X, bool VEC>
 static cudaError_t backward_shape(const NormParams& p, cudaStream_t s) {
+  if constexpr (!VEC) {
+    if (p.cols <= 2048) return backward_launch<X, false, 1, kNormThreads, 2, 1, 1, true>(p, s);
+    if (p.cols <= 4096) return backward_launch<X, false, 2, kNormThreads, 2, 2, 1, true>(p, s);
+    if (p.cols <= 8192) return backward_launch<X, false, 2, 512, 1, 2, 1, true>(p, s);
+    return backward_launch<X, false, 2, 1024, 1, 1, 1, false>(p, s);
+  }
   constexpr bool B16 = sizeof(X) == 2;
   const bool few = p.rows <= 8ll * p.sms;   // one row at a time
   if (p.cols <= 2048)

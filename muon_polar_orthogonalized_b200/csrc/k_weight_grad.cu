@@ -172,7 +172,7 @@ __device__ __forceinline__ void transpose_pieces(float (&v)[4][8], int lane) {
   }
 }
 
-// 8 columns of one row; vec: 16-byte accesses allowed and cols >= 8.
+// 8 columns of one row; vec: whole accesses allowed (rows_vec) and cols >= 8.
 template <typename G>
 __device__ __forceinline__ void store_piece(G* dst, float (&v)[8], int cols, bool accumulate, bool vec) {
   if (vec) {
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
     const uint32_t tempty0 = sm100::mapa_shared(sm100::smem_u32(tempty), 0);
     const int quad = warp & 3, slice = (warp - 2) >> 2;
     constexpr int CH = C::TK / 32;
-    const bool vec = (static_cast<long long>(p.k) * sizeof(G)) % 16 == 0;   // grad is 16-byte aligned
+    const bool vec = p.k % 8 == 0 && reinterpret_cast<uintptr_t>(p.grad) % (8 * sizeof(G)) == 0;
     int stage = 0, turn = 0;   // ring position of the unit's first stage, and whose it is
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;

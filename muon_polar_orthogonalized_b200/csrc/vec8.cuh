@@ -1,6 +1,5 @@
 // vec8.cuh -- groups of 8 consecutive fp32 or bf16 elements in registers, for
-// the streaming kernels: one 16-byte access (bf16), one of 32 bytes or two of 16
-// (fp32).
+// the streaming kernels: one access of 16 bytes (bf16) or 32 (fp32).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,20 +29,13 @@ struct Raw8 {
   uint4 w[sizeof(T) / 2];
 };
 
-// p 16-byte aligned.  8 fp32 are one whole 32-byte sector per lane where they
-// are aligned to it: two 16-byte accesses would each touch half of every sector.
+// p 16-byte aligned for bf16, 32-byte for fp32: 8 fp32 are one whole sector per
+// lane (two 16-byte accesses would each touch half of every sector).
 template <typename T>
 __device__ __forceinline__ Raw8<T> load_raw8(const T* p) {
   Raw8<T> r;
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-  if constexpr (sizeof(T) == 4) {
-    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-      sm100::ld_global_v8(p, r.w[0], r.w[1]);
-      return r;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) r.w[k] = q[k];
+  if constexpr (sizeof(T) == 4) sm100::ld_global_v8(p, r.w[0], r.w[1]);
+  else r.w[0] = *reinterpret_cast<const uint4*>(p);
   return r;
 }
 template <typename T>
@@ -79,7 +71,6 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-  uint4* q = reinterpret_cast<uint4*>(p);
   if constexpr (sizeof(T) == 2) {
     uint32_t w[4];
 #pragma unroll
@@ -87,16 +78,11 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
       const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
       w[k] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     const uint4 lo = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     const uint4 hi = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-      sm100::st_global_v8(p, lo, hi);
-    } else {
-      q[0] = lo;
-      q[1] = hi;
-    }
+    sm100::st_global_v8(p, lo, hi);
   }
 }
 
