@@ -622,6 +622,7 @@ __device__ __forceinline__ void add_long(const EmbedGradParams& p, uint32_t segs
 // from registers took 118), or the warp's stores where rows are not whole
 // 16-byte units.
 constexpr int kZeroBytes = 8192;
+constexpr int kRowBlocks = 3;   // of the rows kernel per SM
 template <typename G>
 __device__ __forceinline__ void fill_rows(const EmbedGradParams& p, const uint4* zeros) {
   const int lane = threadIdx.x;
@@ -651,7 +652,7 @@ __device__ __forceinline__ void fill_rows(const EmbedGradParams& p, const uint4*
 // the ninth writes zeros: the reads of some rows and the writes of others share
 // the memory's time.
 template <typename D, typename G, bool VEC>
-__global__ void __launch_bounds__(32 * (kEmbWarps + 1), 3) embedding_rows_kernel(const EmbedGradParams p, uint32_t segs,
+__global__ void __launch_bounds__(32 * (kEmbWarps + 1), kRowBlocks) embedding_rows_kernel(const EmbedGradParams p, uint32_t segs,
                                                                                  int lpr) {
   __shared__ float part[kEmbWarps][kSumUnits * 8][32];
   __shared__ __align__(128) uint4 zeros[kZeroBytes / 16];
@@ -671,33 +672,51 @@ __global__ void __launch_bounds__(32 * (kEmbWarps + 1), 3) embedding_rows_kernel
   const uint2* sorted = p.sorted[(p.passes + 1) & 1];
   const int l = threadIdx.x % lpr;
   const uint32_t per_warp = 32 / lpr, count = p.counts->shorts;
-  // Tasks: row pieces of groups of per_warp runs.  The next task's run is read
-  // while one is added, and a run of one token (most are) names it itself, so
-  // that only the row is waited for.
+  // Tasks: row pieces of groups of per_warp runs, BATCH at a time: the runs of
+  // the next batch are read while this one's are added, and a run of one token
+  // (most are) names it itself, so that only the rows are waited for, together.
+  constexpr int BATCH = VEC ? 2 : 1;
   const unsigned long long tasks = static_cast<unsigned long long>((count + per_warp - 1) / per_warp) * segs;
+  const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * kEmbWarps;
   const D* dout = static_cast<const D*>(p.dout);
-  auto task = [&](unsigned long long it, int& c0) -> uint4 {
-    const uint32_t q = it <= 0xffffffffull ? static_cast<uint32_t>(it) / segs : static_cast<uint32_t>(it / segs);
-    c0 = static_cast<int>(it - static_cast<unsigned long long>(q) * segs) * (32 * 8 * kSumUnits);
-    const uint32_t i = q * per_warp + threadIdx.x / lpr;
-    return it < tasks && i < count ? p.shorts[i] : make_uint4(0, 0, 0, 0);   // no run: nothing to do
-  };
-  int c0;
   unsigned long long it = blockIdx.x * kEmbWarps + threadIdx.y;
-  uint4 w = task(it, c0);
-  while (it < tasks) {
-    it += gridDim.x * kEmbWarps;
-    int c0_next;
-    const uint4 w_next = task(it, c0_next);
-    if (w.z > w.y) {
-      Sums<kSumUnits> a = {};
-      add_rows<D, VEC, VEC ? 4 : 2>(w.y, w.z - 1, p.dim, c0, lpr, l, a,
-                                    [&](uint32_t k) { return dout + sorted[k].y * p.dout_ld; });
-      add_rows<D, VEC, 1>(0, 1, p.dim, c0, lpr, l, a, [&](uint32_t) { return dout + w.w * p.dout_ld; });
-      write_row<G, VEC>(p, static_cast<G*>(p.grad) + static_cast<long long>(w.x) * p.dim, c0, lpr, l, a);
+  uint4 w[BATCH];
+  int c0[BATCH];
+  auto runs = [&](uint4 (&w)[BATCH], int (&c0)[BATCH], unsigned long long it) {
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const unsigned long long t = it + k * step;
+      const uint32_t q = t <= 0xffffffffull ? static_cast<uint32_t>(t) / segs : static_cast<uint32_t>(t / segs);
+      c0[k] = static_cast<int>(t - static_cast<unsigned long long>(q) * segs) * (32 * 8 * kSumUnits);
+      const uint32_t i = q * per_warp + threadIdx.x / lpr;
+      w[k] = t < tasks && i < count ? p.shorts[i] : make_uint4(0, 0, 0, 0);   // no run: nothing to do
     }
-    w = w_next;
-    c0 = c0_next;
+  };
+  runs(w, c0, it);
+  while (it < tasks) {
+    RowPiece<D, VEC, kSumUnits> last[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (w[k].z > w[k].y) last[k].load(dout + w[k].w * p.dout_ld, p.dim, c0[k], lpr, l);
+    uint4 w_next[BATCH];
+    int c0_next[BATCH];
+    it += BATCH * step;
+    runs(w_next, c0_next, it);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (w[k].z > w[k].y) {
+        Sums<kSumUnits> a = {};
+        add_rows<D, VEC, VEC ? 4 : 2>(w[k].y, w[k].z - 1, p.dim, c0[k], lpr, l, a,
+                                      [&](uint32_t i) { return dout + sorted[i].y * p.dout_ld; });
+        last[k].add_to(a, p.dim, c0[k], lpr, l);
+        write_row<G, VEC>(p, static_cast<G*>(p.grad) + static_cast<long long>(w[k].x) * p.dim, c0[k], lpr, l, a);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      w[k] = w_next[k];
+      c0[k] = c0_next[k];
+    }
   }
 }
 
@@ -821,7 +840,7 @@ template <typename D, typename G, bool VEC>
 static cudaError_t rows_typed(const EmbedGradParams& p, cudaStream_t s) {
   int lpr = 32;
   while (lpr > 1 && p.dim <= lpr / 2 * 8 * kSumUnits) lpr /= 2;
-  return launch_pdl(embedding_rows_kernel<D, G, VEC>, dim3(3 * p.sms), dim3(32, kEmbWarps + 1), 0, s, p,
+  return launch_pdl(embedding_rows_kernel<D, G, VEC>, dim3(kRowBlocks * p.sms), dim3(32, kEmbWarps + 1), 0, s, p,
                     sum_segments(p.dim), lpr);
 }
 cudaError_t launch_embedding_rows(const EmbedGradParams& p, cudaStream_t s) {
