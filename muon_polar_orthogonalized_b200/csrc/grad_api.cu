@@ -19,12 +19,12 @@ constexpr int64_t kMaxRows = 1ll << 30;      // tokens, activation rows
 constexpr int64_t kMaxVocab = 1ll << 30;
 constexpr int64_t kMaxDim = 65536;           // embedding and matrix widths
 // Measured costs of a weight gradient's parts, in microseconds: a stage (64
-// rows of a tile), a tile's start and drain, the launch that joins shared
+// rows of a tile), a tile's drain, the launch, the launch that joins shared
 // tiles, and each worker's sums written and read.
 struct WgCost {
-  double stage, tile, join, part;
+  double stage, tile, start, join, part;
 };
-constexpr WgCost kWgCost[2] = {{0.40, 6.5, 3.0, 0.02}, {0.66, 11.5, 4.0, 0.10}};   // narrow, wide
+constexpr WgCost kWgCost[2] = {{0.40, 3.8, 3.0, 3.0, 0.03}, {0.70, 8.0, 4.0, 4.0, 0.17}};   // narrow, wide
 constexpr int64_t kMaxTasks = 1ll << 33;     // warps of a launch (8 per block, 2^31 - 1 blocks)
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -140,19 +140,25 @@ WeightWs weight_plan(WeightWs w, int wide, int64_t n, int64_t k) {
   w.tiles_k = (k + kWgTile[wide].k - 1) / kWgTile[wide].k;
   w.tiles = w.tiles_n * w.tiles_k;
   w.cost = 1e300;
+  const double tile_time = w.kblocks * c.stage + c.tile;
   if (w.tiles >= kPairs) {
-    // whole rounds of tiles, but for the last one and what is left after it
+    // whole tiles only, or whole rounds of them but for the last one and what is
+    // left after it, which are dealt out by row blocks
     w.workers = kPairs;
+    w.whole_tiles = static_cast<int>(w.tiles);
+    w.cost = static_cast<double>((w.tiles + kPairs - 1) / kPairs) * tile_time + c.start;
     const int64_t rounds = w.tiles / kPairs;
-    w.whole_tiles = static_cast<int>(w.tiles % kPairs == 0 ? w.tiles : (rounds - 1) * kPairs);
-    const bool even = w.tiles % kPairs == 0;
-    w.cost = static_cast<double>(w.tiles) / kPairs * w.kblocks * c.stage + (even ? rounds : rounds + 1) * c.tile +
-             (even ? 0.0 : c.join + 2 * kPairs * c.part);
+    const double shared = static_cast<double>(w.tiles) / kPairs * w.kblocks * c.stage + (rounds + 1) * c.tile + c.start +
+                          c.join + 2 * kPairs * c.part;
+    if (w.tiles % kPairs != 0 && shared < w.cost) {
+      w.whole_tiles = static_cast<int>((rounds - 1) * kPairs);
+      w.cost = shared;
+    }
   } else {
     // several workers per tile where that is faster
     w.whole_tiles = 0;
     for (int64_t per = 1; per <= std::max<int64_t>(w.kblocks, 1) && w.tiles * per <= kPairs; ++per) {
-      const double cost = static_cast<double>((w.kblocks + per - 1) / per) * c.stage + c.tile +
+      const double cost = static_cast<double>((w.kblocks + per - 1) / per) * c.stage + c.tile + c.start +
                           (per == 1 ? 0.0 : c.join + static_cast<double>(w.tiles * per) * c.part);
       if (cost < w.cost) {
         w.cost = cost;
@@ -160,8 +166,8 @@ WeightWs weight_plan(WeightWs w, int wide, int64_t n, int64_t k) {
       }
     }
   }
-  w.shared = (w.tiles - w.whole_tiles) * w.kblocks % w.workers != 0 ||
-             (w.tiles - w.whole_tiles) * w.kblocks / w.workers % std::max(w.kblocks, 1) != 0;
+  const int64_t blocks = (w.tiles - w.whole_tiles) * w.kblocks;
+  w.shared = w.kblocks > 1 && (blocks % w.workers != 0 || blocks / w.workers % w.kblocks != 0);
   return w;
 }
 WeightWs weight_ws(int64_t rows, int64_t n, int64_t k, int32_t dy_dtype, bool dy_aligned) {
@@ -461,8 +467,9 @@ muon_status muon_checkpoint_weight_grad(const void* dy, int32_t dy_dtype, int64_
       src = base + 256;
       ld = w.pitch;
       st = launched(api_timed_launch(K_WEIGHT_GRAD, s, [&] {
-                      return launch_weight_grad_stage(dy, dy_dtype == MUON_BF16, dy_pitch, base + 256, rows,
-                                                      static_cast<int>(n), static_cast<int>(w.pitch), s);
+                      return launch_weight_grad_stage(dy, dy_dtype == MUON_BF16, rows_vec(dy, dy_dtype, n, dy_pitch),
+                                                      dy_pitch, base + 256, rows, static_cast<int>(n),
+                                                      static_cast<int>(w.pitch), s);
                     }), "weight gradient staging launch");
       if (st != MUON_OK) return st;
     }

@@ -120,8 +120,8 @@ cudaError_t launch_layer_norm_columns(const NormParams& p, cudaStream_t s);
 int layer_norm_grad_blocks(long long rows, int cols, int sms);
 cudaError_t launch_checkpoint_pack(const CkptParams& p, cudaStream_t s);
 cudaError_t launch_checkpoint_unpack(const CkptParams& p, cudaStream_t s);
-cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,
-                                     int pitch, cudaStream_t s);
+cudaError_t launch_weight_grad_stage(const void* dy, int bf16, int vec, long long dy_ld, void* out, long long rows,
+                                     int n, int pitch, cudaStream_t s);
 cudaError_t launch_weight_grad_tc(const WeightGradTc& p, cudaStream_t s);
 cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s);
 

@@ -172,22 +172,33 @@ __device__ __forceinline__ void transpose_pieces(float (&v)[4][8], int lane) {
   }
 }
 
-// 8 columns of one row; vec: whole accesses allowed (rows_vec) and cols >= 8.
-template <typename G>
-__device__ __forceinline__ void store_piece(G* dst, float (&v)[8], int cols, bool accumulate, bool vec) {
-  if (vec) {
-    if (accumulate) {
-      float o[8];
-      load8(dst, o);
+// The whole block transposed, lane = column, for rows that whole accesses do not
+// fit: single stores then adjoin across the warp (one row per instruction).
+__device__ __forceinline__ void transpose_block(float (&v)[32], int lane) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += o[k];
+  for (int b = 16; b > 0; b >>= 1) {
+    const bool up = lane & b;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & b) continue;
+      const float send = up ? v[i] : v[i | b];
+      const float recv = __shfl_xor_sync(0xffffffffu, send, b);
+      if (up) v[i] = recv;
+      else v[i | b] = recv;
     }
-    store8(dst, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < cols) dst[k] = from_f32<G>(v[k] + (accumulate ? to_f32(dst[k]) : 0.f));
   }
+}
+
+// dst <- (dst +) 8 columns of one row, accessed whole.
+template <typename G>
+__device__ __forceinline__ void store_piece(G* dst, float (&v)[8], bool accumulate) {
+  if (accumulate) {
+    float o[8];
+    load8(dst, o);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += o[k];
+  }
+  store8(dst, v);
 }
 
 __device__ __forceinline__ void wg_timeout(unsigned int* status, volatile int* abort_flag) {
@@ -449,22 +460,39 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
         uint32_t r[32];
         sm100::tmem_ld32_async(tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c * 32), r);
         sm100::tmem_wait_ld(r);
-        float v[4][8];
+        // features 1 and 2 of every four back in place
+        auto sum = [&](int k) { return __uint_as_float(r[(k & 3) == 1 ? k + 1 : (k & 3) == 2 ? k - 1 : k]); };
+        const int row0 = u.n0 + (c / CH) * 256 + rank * 128 + quad * 32;
+        G* grad = static_cast<G*>(p.grad);
+        if (vec || u.slot >= 0) {
+          float v[4][8];
 #pragma unroll
-        for (int k = 0; k < 32; ++k)   // features 1 and 2 of every four back in place
-          v[k >> 3][k & 7] = __uint_as_float(r[(k & 3) == 1 ? k + 1 : (k & 3) == 2 ? k - 1 : k]);
-        transpose_pieces(v, lane);
-        const int row0 = u.n0 + (c / CH) * 256 + rank * 128 + quad * 32 + (lane & ~3);
-        const int c0 = col + (lane & 3) * 8;
+          for (int k = 0; k < 32; ++k) v[k >> 3][k & 7] = sum(k);
+          transpose_pieces(v, lane);
+          const int c0 = col + (lane & 3) * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = row0 + i;
-          if (row >= p.n) continue;
-          if (u.slot >= 0)
-            store8(p.partial + (static_cast<long long>(u.slot) * C::TN + (row - u.n0)) * C::TK + (c0 - u.k0), v[i]);
-          else
-            store_piece(static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + c0, v[i], p.k - c0,
-                        p.accumulate != 0, vec && c0 + 8 <= p.k);
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + (lane & ~3) + i;
+            if (row >= p.n || c0 >= p.k) continue;
+            if (u.slot >= 0)
+              store8(p.partial + (static_cast<long long>(u.slot) * C::TN + (row - u.n0)) * C::TK + (c0 - u.k0), v[i]);
+            else
+              store_piece(grad + static_cast<long long>(row) * p.k + c0, v[i], p.accumulate != 0);
+          }
+        } else {
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = sum(k);
+          transpose_block(v, lane);
+          if (col + lane < p.k) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (row0 + k >= p.n) break;
+              G* dst = grad + static_cast<long long>(row0 + k) * p.k + col + lane;
+              *dst = from_f32<G>(v[k] + (p.accumulate ? to_f32(*dst) : 0.f));
+            }
+          }
+          __syncwarp();
         }
       }
       sm100::tc_fence_before();
@@ -540,28 +568,33 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
 // n).  fp32: v = p0 + p1 + p2, each the 8 leading significant bits of what is
 // left (cut, not rounded: nothing overflows, and 3 x 8 bits hold all 24);
 // infinities and NaN go to plane 0 alone.
-template <typename D, int PLANES>
+// A lane takes 8 columns, a warp 256 of a row.
+template <typename D, int PLANES, bool VEC>
 __global__ void __launch_bounds__(256) weight_grad_stage_kernel(const D* dy, long long dy_ld, __nv_bfloat16* out,
                                                                 long long rows, int n, int pitch) {
   pdl_launch_dependents();
   pdl_wait();
-  const int per_row = pitch / 2;   // two columns per thread
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const long long t = i / per_row;
-  if (t >= rows) return;
-  const int c = static_cast<int>(i - t * per_row) * 2;
-  float v[2];
+  const long long t = static_cast<long long>(blockIdx.x) * blockDim.z + threadIdx.z;
+  const int c = ((blockIdx.y * blockDim.y + threadIdx.y) * 32 + threadIdx.x) * 8;
+  if (t >= rows || c >= pitch) return;
+  float v[8] = {};
+  if constexpr (VEC) {
+    if (c < n) load8(dy + t * dy_ld + c, v);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) v[k] = c + k < n ? to_f32(dy[t * dy_ld + c + k]) : 0.f;
+    for (int k = 0; k < 8; ++k)
+      if (c + k < n) v[k] = to_f32(dy[t * dy_ld + c + k]);
+  }
 #pragma unroll
   for (int pl = 0; pl < PLANES; ++pl) {
-    uint32_t b[2];
+    uint32_t b[8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 8; ++k) {
       b[k] = isnan(v[k]) ? 0x7fffu : __float_as_uint(v[k]) >> 16;
       v[k] = isfinite(v[k]) ? v[k] - __uint_as_float(b[k] << 16) : 0.f;
     }
-    *reinterpret_cast<uint32_t*>(out + (static_cast<long long>(pl) * rows + t) * pitch + c) = b[0] | (b[1] << 16);
+    *reinterpret_cast<uint4*>(out + (static_cast<long long>(pl) * rows + t) * pitch + c) =
+        make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16));
   }
 }
 
@@ -603,15 +636,18 @@ cudaError_t launch_weight_grad_join(const WeightGradTc& p, cudaStream_t s) {
   return p.grad_bf16 ? join_launch<B, false>(p, s) : join_launch<float, false>(p, s);
 }
 
-cudaError_t launch_weight_grad_stage(const void* dy, int bf16, long long dy_ld, void* out, long long rows, int n,
-                                     int pitch, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((rows * (pitch / 2) + 255) / 256));
+cudaError_t launch_weight_grad_stage(const void* dy, int bf16, int vec, long long dy_ld, void* out, long long rows,
+                                     int n, int pitch, cudaStream_t s) {
+  const unsigned segs = static_cast<unsigned>((pitch + 255) / 256);
+  unsigned wx = 1;
+  while (wx < 8 && wx < segs) wx *= 2;
+  const dim3 block(32, wx, 8 / wx), grid(static_cast<unsigned>((rows + block.z - 1) / block.z), (segs + wx - 1) / wx);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
-  if (bf16)
-    return launch_pdl(weight_grad_stage_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, s,
+  if (bf16)   // bf16 is staged because it cannot be read in whole accesses
+    return launch_pdl(weight_grad_stage_kernel<__nv_bfloat16, 1, false>, grid, block, 0, s,
                       static_cast<const __nv_bfloat16*>(dy), dy_ld, o, rows, n, pitch);
-  return launch_pdl(weight_grad_stage_kernel<float, 3>, grid, dim3(256), 0, s, static_cast<const float*>(dy), dy_ld, o,
-                    rows, n, pitch);
+  return launch_pdl(vec ? weight_grad_stage_kernel<float, 3, true> : weight_grad_stage_kernel<float, 3, false>, grid,
+                    block, 0, s, static_cast<const float*>(dy), dy_ld, o, rows, n, pitch);
 }
 
 }  // namespace muon
