@@ -342,11 +342,13 @@ muon_status adamw_step_scheduled(const adamw_group* groups, int n_groups,
  *   Workspace    256-byte aligned, at least the bytes the *_workspace_size
  *                function of the same arguments gives (0 on invalid ones);
  *                scratch, no initialisation.  Calls that share one must be
- *                ordered.
+ *                ordered.  muon_query_status reads its status word: the
+ *                weight gradient's waits are bounded and report there.
  *   Aliasing     outputs overlap no input, but y may be x and dx may be dy or
  *                x (same pointer, pitch and type).
  *   Sizes        rows, n <= 2^30; vocab <= 2^30; widths <= 65536 (layer norm
- *                16384, else MUON_ERR_UNSUPPORTED).  Zero rows are a valid
+ *                16384, else MUON_ERR_UNSUPPORTED); rows * pitch <= 2^40, and
+ *                vocab or n times ceil(dim / 128) <= 2^33.  Zero rows are a valid
  *                call: gradients are then zeros, or left as they are when
  *                accumulating.
  */
@@ -411,8 +413,9 @@ muon_status muon_layer_norm_backward(const void* dy, int64_t dy_pitch, const voi
  * magnitude to at most 448 (127 for a block of zeros).  Codes are rounded to
  * nearest even: an error of at most 2^-4 of the value, or 2^-10 times the
  * power of two for the smallest.  A block with an infinity or NaN has exponent
- * 255 and stands for NaN throughout.  Restored values are exact in bf16 and
- * fp32 (values that round up past the type's largest become infinite).
+ * 255 and stands for NaN throughout; the codes 0x7f and 0xff (the format's
+ * NaN) occur in such blocks only.  Restored values are exact in bf16 and fp32
+ * (values that round up past the type's largest become infinite).
  */
 muon_status muon_checkpoint_pack(const void* x, int32_t x_dtype, int64_t x_pitch, int64_t rows,
                                  int64_t cols, uint8_t* codes, int64_t code_pitch,
@@ -456,8 +459,9 @@ muon_status adamw_query_status(muon_stream_t stream);
 
 /*
  * Synchronises `stream`, reads the workspace status word written by the
- * device during the last muon_step / muon_orthogonalize on it, and returns
- * MUON_OK or the recorded error (MUON_ERR_TIMEOUT).
+ * device during the last muon_step / muon_orthogonalize (or gradient-making
+ * call with a workspace) on it, and returns MUON_OK or the recorded error
+ * (MUON_ERR_TIMEOUT).
  */
 muon_status muon_query_status(const void* workspace, muon_stream_t stream);
 

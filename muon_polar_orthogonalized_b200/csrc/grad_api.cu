@@ -236,7 +236,8 @@ muon_status muon_embedding_grad(const void* dout, int32_t dout_dtype, int64_t do
     if ((st = check_workspace(workspace, workspace_bytes, w.total)) != MUON_OK) return st;
     int sms;
     if ((st = api_device(&sms)) != MUON_OK) return st;
-    if (n == 0 && accumulate) return MUON_OK;
+    if (n == 0 && accumulate)
+      return launched(cudaMemsetAsync(workspace, 0, 4, reinterpret_cast<cudaStream_t>(stream)), "clear status");
     EmbedGradParams p = {};
     p.dout = dout;
     p.ids = ids;

@@ -9,6 +9,7 @@ all arithmetic runs in the CUDA library.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Dict, List, Optional, Sequence
 
 import torch
@@ -96,14 +97,15 @@ class MuonAdamW:
         parts = list(grad) if isinstance(grad, (list, tuple)) else [grad]
         if not parts or not all(isinstance(f, (api.LinearGrad, api.EmbeddingGrad)) for f in parts):
             raise ValueError("a gradient is a tensor, a LinearGrad or EmbeddingGrad, or a list of these")
-        if param.grad is None:
-            param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
-                                          requires_grad=False)
-        need = max(f.workspace_size(param.grad) for f in parts)
-        if self._factor_workspace is None or self._factor_workspace.numel() < need:
-            self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
-            if stream is not None:
-                self._factor_workspace.record_stream(stream)
+        # allocated on the stream that writes them, so that memory freed on
+        # another stream is not reused while it is still read there
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            if param.grad is None:
+                param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
+                                              requires_grad=False)
+            need = max(f.workspace_size(param.grad) for f in parts)
+            if self._factor_workspace is None or self._factor_workspace.numel() < need:
+                self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
         for k, f in enumerate(parts):
             f.write(param.grad, self._factor_workspace, accumulate=k > 0, stream=stream)
         return param.grad

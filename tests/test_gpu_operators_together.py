@@ -269,6 +269,24 @@ def test_offsets_beyond_32_bits(dev):
     assert bool((grad[:, ::2] == 3.0).all()) and bool((grad[:, 1::2] == -3.0).all())
 
 
+def test_status_words_are_cleared(dev):
+    """Every call with a workspace leaves a status that reads as success."""
+    b = Block(dev)
+    b.forward()
+    b.backward_norm()
+    none = torch.empty(0, dtype=torch.int64, device=dev)
+    empty = api.new_checkpoint(0, b.dim, dev)
+    for call in (lambda w: api.muon_checkpoint_weight_grad(b.dy, b.ckpt, b.dweight, w),
+                 lambda w: api.muon_checkpoint_weight_grad(b.dy[:0], empty, b.dweight, w, accumulate=True),
+                 lambda w: api.muon_embedding_grad(b.dx, b.ids, b.dtable, w),
+                 lambda w: api.muon_embedding_grad(b.dx[:0], none, b.dtable, w, accumulate=True),
+                 lambda w: api.muon_embedding_grad(b.dx[:0], none, b.dtable, w),
+                 lambda w: api.muon_layer_norm_backward(b.dnorm, b.x, b.gain, b.mean, b.rstd, b.dx, b.dgain, b.dbias, w)):
+        b.ws.fill_(0xFF)
+        call(b.ws)
+        assert api.muon_query_status(b.ws) == N.MUON_OK
+
+
 def test_profiler_counts_the_operators(dev):
     b = Block(dev)
     api.muon_profiler_reset()
