@@ -13,6 +13,7 @@ pointers are passed through unchecked.
 from __future__ import annotations
 
 import ctypes
+import math
 from ctypes import c_double, c_float, c_int64, c_void_p
 from typing import List, Optional, Sequence, Tuple
 
@@ -294,22 +295,21 @@ def adamw_step_scheduled(groups: Sequence[AdamWSpec], schedule_state, stream=Non
 # device is the current one, shapes walked only where a tensor is strided.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_DTYPE = {torch.float32: N.MUON_F32, torch.bfloat16: N.MUON_BF16}
 
 
-def _device_of(fn: str, *tensors) -> int:
-    """The one CUDA device of (name, tensor) pairs given flat; None is skipped."""
-    dev = -1
-    for i in range(1, len(tensors), 2):
-        t = tensors[i]
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{fn}: {tensors[i - 1]} is not a CUDA tensor")
-        if dev < 0:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"{fn}: {tensors[i - 1]} is on cuda:{d}, {tensors[0]} on cuda:{dev}")
+def _device_of(fn: str, names: str, *tensors) -> int:
+    """The one CUDA device of the tensors (names: theirs, in order); None is skipped."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            bad = names.split()[next(i for i, x in enumerate(tensors)
+                                     if x is not None and (x.get_device() < 0 or x.get_device() != dev))]
+            where = [f"{n} on {x.device}" for n, x in zip(names.split(), tensors) if x is not None]
+            if any(x is not None and x.get_device() < 0 for x in tensors):
+                raise ValueError(f"{fn}: {bad} is not a CUDA tensor, or the others are not ({', '.join(where)})")
+            raise ValueError(f"{fn}: {bad} is on another device ({', '.join(where)})")
     return dev
 
 
@@ -322,7 +322,7 @@ def _launch(fn: str, dev: int, stream, call, *args) -> None:
         raise ValueError(f"{fn}: stream of {stream.device}, tensors on cuda:{dev}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = call(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -332,12 +332,10 @@ def _launch(fn: str, dev: int, stream, call, *args) -> None:
 
 
 def _dtype_code(fn: str, name: str, t) -> int:
-    d = t.dtype
-    if d is torch.bfloat16:
-        return N.MUON_BF16
-    if d is torch.float32:
-        return N.MUON_F32
-    raise ValueError(f"{fn}: {name} must be fp32 or bf16, got {d}")
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{fn}: {name} must be fp32 or bf16, got {t.dtype}")
+    return code
 
 
 def _rows(fn: str, name: str, t, cols: Optional[int] = None, rows: Optional[int] = None):
@@ -347,12 +345,7 @@ def _rows(fn: str, name: str, t, cols: Optional[int] = None, rows: Optional[int]
     if not shape:
         raise ValueError(f"{fn}: {name} has no dimension")
     c = shape[-1]
-    if len(shape) == 2:
-        r = shape[0]
-    else:
-        r = 1
-        for d in shape[:-1]:
-            r *= d
+    r = shape[0] if len(shape) == 2 else math.prod(shape[:-1])
     if (cols is not None and c != cols) or (rows is not None and r != rows):
         raise ValueError(f"{fn}: {name} {tuple(shape)} is not {'*' if rows is None else rows} rows of "
                          f"{'*' if cols is None else cols}")
@@ -414,7 +407,7 @@ def muon_embedding_forward(table, ids, out, scale: float = 1.0, stream=None) -> 
     [0, vocab).  table: fp32 or bf16 [vocab, dim]; ids: int32 or int64, any
     shape; out: fp32 or bf16 [*ids.shape, dim] (rows may be strided)."""
     fn = "muon_embedding_forward"
-    dev = _device_of(fn, "table", table, "ids", ids, "out", out)
+    dev = _device_of(fn, "table ids out", table, ids, out)
     vocab, dim = _table(fn, "table", table)
     bits, n = _ids(fn, ids)
     _, _, pitch = _rows(fn, "out", out, dim, n)
@@ -431,7 +424,7 @@ def muon_embedding_grad(dout, ids, grad, workspace, scale: float = 1.0, accumula
     """grad[v] <- (grad[v] +) scale * sum of dout[t] over t with ids[t] = v.
     dout: fp32 or bf16 [*ids.shape, dim]; grad: fp32 or bf16 [vocab, dim]."""
     fn = "muon_embedding_grad"
-    dev = _device_of(fn, "dout", dout, "ids", ids, "grad", grad, "workspace", workspace)
+    dev = _device_of(fn, "dout ids grad workspace", dout, ids, grad, workspace)
     vocab, dim = _table(fn, "grad", grad)
     bits, n = _ids(fn, ids)
     _, _, pitch = _rows(fn, "dout", dout, dim, n)
@@ -445,7 +438,7 @@ def muon_layer_norm_forward(x, gain, bias, y, mean, rstd, eps: float = 1e-5, str
     rstd (fp32, one per row) are written for the backward pass.  x, y: fp32 or
     bf16; gain, bias: fp32 [cols] (bias may be None)."""
     fn = "muon_layer_norm_forward"
-    dev = _device_of(fn, "x", x, "gain", gain, "bias", bias, "y", y, "mean", mean, "rstd", rstd)
+    dev = _device_of(fn, "x gain bias y mean rstd", x, gain, bias, y, mean, rstd)
     rows, cols, xp = _rows(fn, "x", x)
     _, _, yp = _rows(fn, "y", y, cols, rows)
     _dense(fn, "gain", gain, cols, cols, torch.float32)
@@ -468,8 +461,7 @@ def muon_layer_norm_backward(dy, x, gain, mean, rstd, dx, dgain, dbias, workspac
     and dgain and dbias (fp32 or bf16 [cols]; dbias may be None), overwritten
     or added to."""
     fn = "muon_layer_norm_backward"
-    dev = _device_of(fn, "dy", dy, "x", x, "gain", gain, "mean", mean, "rstd", rstd, "dx", dx, "dgain", dgain,
-                     "dbias", dbias, "workspace", workspace)
+    dev = _device_of(fn, "dy x gain mean rstd dx dgain dbias workspace", dy, x, gain, mean, rstd, dx, dgain, dbias, workspace)
     rows, cols, xp = _rows(fn, "x", x)
     _, _, dyp = _rows(fn, "dy", dy, cols, rows)
     _, _, dxp = _rows(fn, "dx", dx, cols, rows)
@@ -522,7 +514,7 @@ def muon_checkpoint_pack(x, ckpt: Checkpoint, stream=None) -> None:
     """Fill ckpt from x, fp32 or bf16 [..., cols] (rows may be strided)."""
     fn = "muon_checkpoint_pack"
     codes, exps = ckpt.codes, ckpt.exponents
-    dev = _device_of(fn, "x", x, "codes", codes, "exponents", exps)
+    dev = _device_of(fn, "x codes exponents", x, codes, exps)
     rows, cols, pitch = _rows(fn, "x", x, ckpt.cols, codes.shape[0])
     _launch(fn, dev, stream, N.lib().muon_checkpoint_pack, x.data_ptr(), _dtype_code(fn, "x", x), pitch, rows, cols,
             codes.data_ptr(), codes.shape[1], exps.data_ptr())
@@ -532,7 +524,7 @@ def muon_checkpoint_unpack(ckpt: Checkpoint, out, stream=None) -> None:
     """out <- the values the checkpoint stands for (fp32 or bf16, both exact)."""
     fn = "muon_checkpoint_unpack"
     codes, exps = ckpt.codes, ckpt.exponents
-    dev = _device_of(fn, "codes", codes, "exponents", exps, "out", out)
+    dev = _device_of(fn, "codes exponents out", codes, exps, out)
     rows, cols, pitch = _rows(fn, "out", out, ckpt.cols, codes.shape[0])
     _launch(fn, dev, stream, N.lib().muon_checkpoint_unpack, codes.data_ptr(), codes.shape[1], exps.data_ptr(), rows,
             cols, out.data_ptr(), _dtype_code(fn, "out", out), pitch)
@@ -553,7 +545,7 @@ def muon_checkpoint_weight_grad(dy, ckpt: Checkpoint, grad, workspace, accumulat
     dy (fp32 or bf16 [..., n]) and the checkpoint of x [rows, k]."""
     fn = "muon_checkpoint_weight_grad"
     codes, exps = ckpt.codes, ckpt.exponents
-    dev = _device_of(fn, "dy", dy, "codes", codes, "exponents", exps, "grad", grad, "workspace", workspace)
+    dev = _device_of(fn, "dy codes exponents grad workspace", dy, codes, exps, grad, workspace)
     rows, n, pitch = _rows(fn, "dy", dy, None, codes.shape[0])
     _dense(fn, "grad", grad, n * ckpt.cols, ckpt.cols)
     _launch(fn, dev, stream, N.lib().muon_checkpoint_weight_grad, dy.data_ptr(), _dtype_code(fn, "dy", dy), pitch, rows,

@@ -775,6 +775,8 @@ static cudaError_t sort_limit(int* limit) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && (*limit = known[dev].load(std::memory_order_relaxed)) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(embedding_sort_kernel<ONE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(16);
   cfg.blockDim = dim3(kSortThreads);
@@ -794,10 +796,9 @@ static cudaError_t sort_limit(int* limit) {
 }
 template <bool ONE>
 static cudaError_t sort_launch(const EmbedGradParams& p, unsigned nb, cudaStream_t s) {
-  auto kern = embedding_sort_kernel<ONE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  constexpr auto kern = embedding_sort_kernel<ONE>;
   int limit = 8;
+  cudaError_t e = allow_smem<kern>(kSortSmem);
   if (e == cudaSuccess) e = sort_limit<ONE>(&limit);
   if (e != cudaSuccess) return e;
   if (nb > static_cast<unsigned>(limit)) {
@@ -822,8 +823,7 @@ static cudaError_t sort_launch(const EmbedGradParams& p, unsigned nb, cudaStream
 }
 cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   if (p.n <= kSmallSort) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(embedding_sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    const cudaError_t e = allow_smem<embedding_sort_small_kernel>(kSmallSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(embedding_sort_small_kernel, dim3(p.accumulate ? 1 : p.sms), dim3(kSortThreads), kSmallSmem, s, p);
   }

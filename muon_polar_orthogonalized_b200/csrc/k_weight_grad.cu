@@ -601,8 +601,8 @@ __global__ void __launch_bounds__(256) weight_grad_stage_kernel(const D* dy, lon
 // ---------------------------------------------------------------- launchers
 template <typename G, bool WIDE>
 static cudaError_t tc_launch(const WeightGradTc& p, cudaStream_t s) {
-  auto kern = weight_grad_tc_kernel<G, WIDE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WgCfg<WIDE>::SMEM);
+  constexpr auto kern = weight_grad_tc_kernel<G, WIDE>;
+  const cudaError_t e = allow_smem<kern>(WgCfg<WIDE>::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(WG_THREADS);

@@ -146,7 +146,7 @@ def ids(n, dtype=torch.int64):
 
 @pytest.mark.parametrize("match,call", [
     ("not a CUDA", lambda: api.muon_embedding_forward(torch.zeros(4, 8), ids(3), fake(3, 8))),
-    ("cuda:1", lambda: api.muon_embedding_forward(fake(4, 8), ids(3), fake(3, 8, on=1))),
+    ("another device", lambda: api.muon_embedding_forward(fake(4, 8), ids(3), fake(3, 8, on=1))),
     ("table", lambda: api.muon_embedding_forward(fake(4, 2, 4), ids(3), fake(3, 8))),
     ("table", lambda: api.muon_embedding_forward(fake(4, 16)[:, :8], ids(3), fake(3, 8))),
     ("table must be fp32 or bf16", lambda: api.muon_embedding_forward(fake(4, 8, dtype=torch.float16), ids(3), fake(3, 8))),
