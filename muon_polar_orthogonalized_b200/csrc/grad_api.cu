@@ -147,11 +147,16 @@ WeightWs weight_plan(WeightWs w, int wide, int64_t n, int64_t k) {
     w.workers = kPairs;
     w.whole_tiles = static_cast<int>(w.tiles);
     w.cost = static_cast<double>((w.tiles + kPairs - 1) / kPairs) * tile_time + c.start;
-    const int64_t rounds = w.tiles / kPairs;
+    const int64_t rounds = w.tiles / kPairs, left = w.tiles % kPairs;
+    // what is left joins the last round where it is little (else each of its
+    // tiles would be cut into many runs); where it is much, the rounds before
+    // it keep their rows in step and share them in L2 (16384 x 4096 x 4096, 128
+    // tiles: 434 us with both rounds in runs)
+    const int64_t whole_rounds = 2 * left >= kPairs ? rounds : rounds - 1;
     const double shared = static_cast<double>(w.tiles) / kPairs * w.kblocks * c.stage + (rounds + 1) * c.tile + c.start +
                           c.join + 2 * kPairs * c.part;
-    if (w.tiles % kPairs != 0 && shared < w.cost) {
-      w.whole_tiles = static_cast<int>((rounds - 1) * kPairs);
+    if (left != 0 && shared < w.cost) {
+      w.whole_tiles = static_cast<int>(whole_rounds * kPairs);
       w.cost = shared;
     }
   } else {

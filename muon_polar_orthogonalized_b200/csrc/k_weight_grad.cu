@@ -514,7 +514,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
 
 // grad (+)= the runs' sums of each tile that several workers share, in the
 // order of their rows.  Block (b, y): the tile that the start of worker b + 1's
-// run lies inside, if it is the first start inside it; 1024 elements.
+// run lies inside, if it is the first start inside it; 4096 elements, kJoinRows
+// rows per thread so that their loads are in flight together.
+constexpr int kJoinRows = 4;
 template <typename G, bool WIDE>
 __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_constant__ WeightGradTc p) {
   using C = WgCfg<WIDE>;
@@ -527,40 +529,53 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
   if (at == t0 || wg_run(p, w1 - 1) > t0) return;
   int n0, k0;
   wg_tile<WIDE>(p, p.whole_tiles + t, n0, k0);
-  constexpr int QUADS = C::TK / 4;   // threads per row
-  const int r = blockIdx.y * (256 / QUADS) + threadIdx.x / QUADS, c = (threadIdx.x % QUADS) * 4;
-  const int row = n0 + r, col = k0 + c;
-  if (row >= p.n || col >= p.k) return;
-  float s[4] = {};
   int w_end = w1 + 1;
   while (w_end < p.workers && wg_run(p, w_end) < t1) ++w_end;
-#pragma unroll 4
+  // slot 0 of a worker holds the tile its run starts in: of the first worker
+  // here only if its run starts with the tile
+  const int first_slot = 2 * (w1 - 1) + (wg_run(p, w1 - 1) >= t0 ? 0 : 1);
+  constexpr int QUADS = C::TK / 4;   // threads per row
+  constexpr int ROWS = 256 / QUADS;  // rows at a time
+  const int c = (threadIdx.x % QUADS) * 4, col = k0 + c;
+  if (col >= p.k) return;
+  float s[kJoinRows][4] = {};
+  const float* part = p.partial + static_cast<long long>(blockIdx.y * kJoinRows * ROWS + threadIdx.x / QUADS) * C::TK + c;
+  constexpr long long SLOT = static_cast<long long>(C::TN) * C::TK;
   for (int w = w1 - 1; w < w_end; ++w) {
-    const int slot = 2 * w + (wg_run(p, w) >= t0 ? 0 : 1);   // 0: the tile its run starts in
-    const float4 v = *reinterpret_cast<const float4*>(
-        p.partial + (static_cast<long long>(slot) * C::TN + r) * C::TK + c);
-    s[0] += v.x;
-    s[1] += v.y;
-    s[2] += v.z;
-    s[3] += v.w;
-  }
-  G* out = static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + col;
-  if (col + 4 <= p.k && p.k % 4 == 0) {
-    if constexpr (sizeof(G) == 4) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.accumulate) o = *reinterpret_cast<const float4*>(out);
-      *reinterpret_cast<float4*>(out) = make_float4(o.x + s[0], o.y + s[1], o.z + s[2], o.w + s[3]);
-    } else {
-      if (p.accumulate)
+    const float* src = part + (w == w1 - 1 ? first_slot : 2 * w) * SLOT;
+    float4 v[kJoinRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] += to_f32(out[k]);
-      const __nv_bfloat162 a = __floats2bfloat162_rn(s[0], s[1]), b = __floats2bfloat162_rn(s[2], s[3]);
-      *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    for (int i = 0; i < kJoinRows; ++i) v[i] = *reinterpret_cast<const float4*>(src + i * ROWS * C::TK);
+#pragma unroll
+    for (int i = 0; i < kJoinRows; ++i) {
+      s[i][0] += v[i].x;
+      s[i][1] += v[i].y;
+      s[i][2] += v[i].z;
+      s[i][3] += v[i].w;
     }
-  } else {
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (col + k < p.k) out[k] = from_f32<G>(s[k] + (p.accumulate ? to_f32(out[k]) : 0.f));
+  for (int i = 0; i < kJoinRows; ++i) {
+    const int row = n0 + (blockIdx.y * kJoinRows + i) * ROWS + threadIdx.x / QUADS;
+    if (row >= p.n) break;
+    G* out = static_cast<G*>(p.grad) + static_cast<long long>(row) * p.k + col;
+    if (p.k % 4 == 0) {   // grad is 16-byte aligned
+      if constexpr (sizeof(G) == 4) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.accumulate) o = *reinterpret_cast<const float4*>(out);
+        *reinterpret_cast<float4*>(out) = make_float4(o.x + s[i][0], o.y + s[i][1], o.z + s[i][2], o.w + s[i][3]);
+      } else {
+        if (p.accumulate)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[i][k] += to_f32(out[k]);
+        const __nv_bfloat162 a = __floats2bfloat162_rn(s[i][0], s[i][1]), b = __floats2bfloat162_rn(s[i][2], s[i][3]);
+        *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (col + k < p.k) out[k] = from_f32<G>(s[i][k] + (p.accumulate ? to_f32(out[k]) : 0.f));
+    }
   }
 }
 
@@ -622,7 +637,7 @@ static cudaError_t tc_launch(const WeightGradTc& p, cudaStream_t s) {
 }
 template <typename G, bool WIDE>
 static cudaError_t join_launch(const WeightGradTc& p, cudaStream_t s) {
-  const dim3 grid(p.workers - 1, WgCfg<WIDE>::TN * WgCfg<WIDE>::TK / 1024);
+  const dim3 grid(p.workers - 1, WgCfg<WIDE>::TN * WgCfg<WIDE>::TK / (1024 * kJoinRows));
   return launch_pdl(weight_grad_join_kernel<G, WIDE>, grid, dim3(256), 0, s, p);
 }
 cudaError_t launch_weight_grad_tc(const WeightGradTc& p, cudaStream_t s) {
