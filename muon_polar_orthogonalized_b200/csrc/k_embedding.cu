@@ -796,9 +796,9 @@ static cudaError_t sort_limit(int* limit) {
 }
 template <bool ONE>
 static cudaError_t sort_launch(const EmbedGradParams& p, unsigned nb, cudaStream_t s) {
-  constexpr auto kern = embedding_sort_kernel<ONE>;
+  const auto kern = embedding_sort_kernel<ONE>;
   int limit = 8;
-  cudaError_t e = allow_smem<kern>(kSortSmem);
+  cudaError_t e = allow_smem(kern, kSortSmem);
   if (e == cudaSuccess) e = sort_limit<ONE>(&limit);
   if (e != cudaSuccess) return e;
   if (nb > static_cast<unsigned>(limit)) {
@@ -823,7 +823,7 @@ static cudaError_t sort_launch(const EmbedGradParams& p, unsigned nb, cudaStream
 }
 cudaError_t launch_embedding_sort(const EmbedGradParams& p, cudaStream_t s) {
   if (p.n <= kSmallSort) {
-    const cudaError_t e = allow_smem<embedding_sort_small_kernel>(kSmallSmem);
+    const cudaError_t e = allow_smem(embedding_sort_small_kernel, kSmallSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(embedding_sort_small_kernel, dim3(p.accumulate ? 1 : p.sms), dim3(kSortThreads), kSmallSmem, s, p);
   }

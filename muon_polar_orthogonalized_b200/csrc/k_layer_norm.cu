@@ -517,7 +517,6 @@ __global__ void __launch_bounds__(32 * kColThreads) layer_norm_column_kernel(con
 
 // ---------------------------------------------------------------- launchers
 namespace {
-constexpr int kRingBytes = 192 * 1024;   // the largest ring: 1024 threads of three bf16 rows' x and dy
 int round32(int x) { return (x + 31) / 32 * 32; }
 // Threads and groups of a block for rows of `units` 8-column units.
 dim3 norm_block(int units_per_thread, int cols) {
@@ -533,10 +532,10 @@ static cudaError_t forward_launch(const NormParams& p, cudaStream_t s) {
   dim3 block = norm_block(UNITS, p.cols);
   // a block of several groups only where there are rows for every SM
   while (block.y > 1 && static_cast<long long>(block.y) * R * p.sms > p.rows) block.y = (block.y + 1) / 2;
-  constexpr auto kern = layer_norm_kernel<X, Y, VEC, UNITS, MAXT, MINB, R, K, HOLD>;
+  const auto kern = layer_norm_kernel<X, Y, VEC, UNITS, MAXT, MINB, R, K, HOLD>;
   const size_t smem = VEC ? static_cast<size_t>(K) * R * UNITS * 8 * sizeof(X) * block.x * block.y : 0;
   if (smem > 32 * 1024) {   // beyond the default limit of 48 KB with the static part
-    const cudaError_t e = allow_smem<kern>(kRingBytes);
+    const cudaError_t e = allow_smem(kern, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   const long long per = static_cast<long long>(block.y) * R;
@@ -594,11 +593,11 @@ int layer_norm_grad_blocks(long long rows, int cols, int sms) {
 template <typename X, bool VEC, int UNITS, int MAXT, int MINB, int R, int K, bool HOLD>
 static cudaError_t backward_launch(const NormParams& p, cudaStream_t s) {
   const dim3 block = norm_block(UNITS, p.cols);
-  constexpr auto kern = layer_norm_grad_kernel<X, VEC, UNITS, MAXT, MINB, R, K, HOLD>;
+  const auto kern = layer_norm_grad_kernel<X, VEC, UNITS, MAXT, MINB, R, K, HOLD>;
   size_t smem = VEC ? static_cast<size_t>(K) * R * 2 * UNITS * 8 * sizeof(X) * block.x * block.y : 0;
   if (block.y > 1) smem = smem > static_cast<size_t>(8) * p.cols ? smem : static_cast<size_t>(8) * p.cols;
   if (smem > 32 * 1024) {
-    const cudaError_t e = allow_smem<kern>(kRingBytes);
+    const cudaError_t e = allow_smem(kern, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, dim3(p.blocks), block, smem, s, p);

@@ -616,8 +616,8 @@ __global__ void __launch_bounds__(256) weight_grad_stage_kernel(const D* dy, lon
 // ---------------------------------------------------------------- launchers
 template <typename G, bool WIDE>
 static cudaError_t tc_launch(const WeightGradTc& p, cudaStream_t s) {
-  constexpr auto kern = weight_grad_tc_kernel<G, WIDE>;
-  const cudaError_t e = allow_smem<kern>(WgCfg<WIDE>::SMEM);
+  const auto kern = weight_grad_tc_kernel<G, WIDE>;
+  const cudaError_t e = allow_smem(kern, WgCfg<WIDE>::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(WG_THREADS);

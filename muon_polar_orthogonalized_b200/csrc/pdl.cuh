@@ -17,8 +17,6 @@
 #pragma once
 #include <cuda_runtime.h>
 
-#include <atomic>
-#include <cstdint>
 #include <utility>
 
 namespace muon {
@@ -29,19 +27,10 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 
 // Lets a kernel use up to `bytes` of dynamic shared memory on the current
-// device: set once per kernel and device, since the call costs as much as a
-// small launch's other host work.
-template <auto Kernel>
-inline cudaError_t allow_smem(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
+// device (set before each launch: 0.06 us, and a reset device needs it again).
+template <typename K>
+inline cudaError_t allow_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 // kernel<<<grid, block, smem, s>>>(args...) with the attribute set.
