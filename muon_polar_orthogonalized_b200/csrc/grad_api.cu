@@ -25,7 +25,7 @@ struct WgCost {
   double stage, tile, start, join, part;
 };
 constexpr WgCost kWgCost[2] = {{0.40, 3.8, 3.0, 3.0, 0.03}, {0.70, 8.0, 4.0, 4.0, 0.17}};   // narrow, wide
-constexpr int64_t kMaxTasks = 1ll << 33;     // warps of a launch (8 per block, 2^31 - 1 blocks)
+constexpr int64_t kMaxTasks = 1ll << 33;     // 128-column pieces of an embedding's rows
 
 bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

@@ -20,20 +20,17 @@
 // 256x256x16 MMAs, two per 16 rows (one for each half of the dy columns), into
 // one 512-column accumulator: restored codes are used for 512 columns of dy,
 // which leaves the sixteen warps 1024 tensor-pipe cycles per stage.  The same
-// sixteen warps write the finished tile.  Measured: 1.46 PFLOP/s at 16384 x
-// 14336 x 4096 (1.32 ms, 1.08 of the measured sustained bf16 product, 0.90 of
-// its burst), 1.25 at 16384 x 1024 x 4096.  Where there are few tiles, or few
+// sixteen warps write the finished tile.  Measured: 1.53 PFLOP/s at 16384 x
+// 14336 x 4096 (1.26 ms, 1.13 of the measured sustained bf16 product, 0.95 of
+// its burst; 1.30 in a long loop, at the power cap), 1.32 at 16384 x 1024 x 4096.  Where there are few tiles, or few
 // rows, a tile's start and drain (11 us) outweigh its product, and tiles of
 // 256 by 128 are used, on which two groups of eight warps take the stages in
-// turn: 12.0 us against 20.2 at 777 x 1664 x 768, but 0.65 PFLOP/s at the
-// large shapes.  The choice is by the estimated time (grad_api.cu).
+// turn: 11.4 us against 19.3 at 777 x 1664 x 768 and 16.3 against 22.2 at 4096 x
+// 768 x 768, but 139 against 98 at 16384 x 1664 x 1664 and 0.74 PFLOP/s at
+// 16384 x 14336 x 4096.  The choice is by the estimated time (grad_api.cu).
 //   warp 0: TMA producer   warp 1: MMA issuer (+ TMEM owner)
 //   warps 2-17: codes to bf16, then the tile's epilogue
-// Three instructions turn two codes into two bf16 and a packed multiply
-// finishes them: the code's exponent and mantissa bits, moved to the low end
-// of bf16's exponent and the high end of its mantissa, read as the value times
-// 2^-120 (bf16 subnormals and the code's line up), so one exact multiply by a
-// power of two remains.  Bytes 1 and 3 of a word of four codes need no move to
+// How codes become bf16 is in e4m3.cuh.  Bytes 1 and 3 of a word of four codes need no move to
 // their halves, so features 1 and 2 of every four change places in the
 // operand, and with them two registers in the epilogue.
 //
