@@ -244,7 +244,7 @@ class AdamWSpec:
         self.params, self.grads, self.exp_avg, self.exp_avg_sq = params, grads, exp_avg, exp_avg_sq
         self.lr, self.beta1, self.beta2, self.eps, self.wd = lr, beta1, beta2, eps, wd
         if grad_dtype is None:
-                    grad_dtype = N.MUON_BF16 if (grads and grads[0].dtype == torch.bfloat16) else N.MUON_F32
+            grad_dtype = N.MUON_BF16 if (grads and grads[0].dtype == torch.bfloat16) else N.MUON_F32
         self.grad_dtype = grad_dtype
 
 

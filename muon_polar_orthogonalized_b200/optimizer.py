@@ -71,6 +71,7 @@ class MuonAdamW:
         dev = self.muon_params[0].device if self.muon_params else torch.device("cuda")
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         self._factor_workspace: Optional[torch.Tensor] = None   # grown by the gradients formed here
+        self._captured_workspaces: List[torch.Tensor] = []        # those that a captured step writes when replayed
 
     def _groups(self, grad_dtypes):
         """Group descriptors, one gradient dtype per shape group."""
@@ -104,8 +105,13 @@ class MuonAdamW:
                 param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
                                               requires_grad=False)
             need = max(f.workspace_size(param.grad) for f in parts)
-            if self._factor_workspace is None or self._factor_workspace.numel() < need:
-                self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
+            ws = self._factor_workspace
+            if ws is None or ws.numel() < need:
+                if ws is not None and ws.is_cuda:   # steps before this one may still be using it, on any stream
+                    ws.record_stream(torch.cuda.current_stream(ws.device))
+                ws = self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
+            if torch.cuda.is_current_stream_capturing() and not any(w is ws for w in self._captured_workspaces):
+                self._captured_workspaces.append(ws)
         for k, f in enumerate(parts):
             f.write(param.grad, self._factor_workspace, accumulate=k > 0, stream=stream)
         return param.grad

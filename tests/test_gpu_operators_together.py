@@ -113,6 +113,45 @@ def test_optimizer_forms_gradients_from_their_factors(dev):
         assert torch.equal(x, y)
 
 
+def test_captured_step_on_factors_outlives_a_larger_one(dev):
+    """A captured step on factors is replayed after an eager step that needed a
+    larger workspace: it forms the same gradients, in memory that nothing else
+    was given meanwhile."""
+    b, big = Block(dev, seed=1), Block(dev, tokens=6000, seed=7)
+    for blk in (b, big):
+        blk.forward()
+        blk.backward_norm()
+    opt = MuonAdamW([b.weight], [dict(params=[b.table], lr=1e-2)], lr=0.02)
+
+    def step(blk, stream=None):
+        opt.step(stream=stream, muon_grads=[api.LinearGrad(blk.dy, blk.ckpt)],
+                 adamw_grads=[[api.EmbeddingGrad(blk.dx, blk.ids, blk.scale)]])
+
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        step(b, side)
+    torch.cuda.synchronize()
+    want = [b.weight.grad.clone(), b.table.grad.clone()]
+    kept = opt._factor_workspace
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(b, side)
+    step(big)
+    assert opt._factor_workspace is not kept
+    size = kept.numel()
+    del kept
+    filler = [torch.full((size,), 0xA5, dtype=torch.uint8, device=dev) for _ in range(16)]
+    b.weight.grad.zero_()
+    b.table.grad.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b.weight.grad, want[0]) and torch.equal(b.table.grad, want[1])
+    assert all(bool((f == 0xA5).all()) for f in filler)
+    del graph
+
+
 def test_optimizer_refuses_other_factors(dev):
     b = Block(dev)
     opt = MuonAdamW([b.weight], [dict(params=[b.table])])

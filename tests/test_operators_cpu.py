@@ -192,3 +192,38 @@ def test_references_agree_with_each_other():
     err = (R.checkpoint_values(codes, exps, 300) - x.double()).abs()
     step = torch.pow(2.0, exps.double() - 127).repeat_interleave(128, 1)[:, :300]
     assert bool((err <= torch.maximum(x.double().abs() * 2.0 ** -4, step * 2.0 ** -10)).all())
+
+
+def test_formed_gradients_keep_the_workspace_of_a_captured_step(monkeypatch):
+    """A captured step writes its workspace at every replay: a later, larger step
+    takes another and must not free it.  Steps that were not captured keep none."""
+    import types
+    from muon_polar_orthogonalized_b200.optimizer import MuonAdamW
+
+    class Factor(api.LinearGrad):
+        def __init__(self, need):
+            self.need = need
+
+        def workspace_size(self, grad):
+            return self.need
+
+        def write(self, grad, workspace, accumulate=False, stream=None):
+            assert workspace.numel() >= self.need
+            grad.fill_(1.0)
+
+    opt = types.SimpleNamespace(_factor_workspace=None, _captured_workspaces=[])
+    param = torch.zeros(4, 4)
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    form = lambda need: MuonAdamW._formed(opt, param, Factor(need), None)
+    form(300)
+    assert opt._captured_workspaces == []
+    capturing[0] = True
+    form(300)
+    form(200)
+    kept = opt._factor_workspace
+    assert len(opt._captured_workspaces) == 1 and opt._captured_workspaces[0] is kept
+    capturing[0] = False
+    form(5000)
+    assert opt._factor_workspace is not kept and opt._captured_workspaces[0] is kept
+    assert len(opt._captured_workspaces) == 1
