@@ -130,10 +130,16 @@ struct Ring {
   __device__ __forceinline__ uint4* slot(int stage, int piece) const {
     return slots + (stage * PER + piece) * threads + tid;
   }
-  // zeros in every slot: the pieces past the row are never copied to
-  __device__ __forceinline__ void clear() const {
+  // zeros in the slots past the row, which `copy` never fills (and only those:
+  // nothing orders a plain store before a later asynchronous copy's).  Split
+  // units alone are read where a half of them is past the row.  OPS operands of
+  // UNITS units, sizeof(T) / 2 pieces each.
+  template <typename C, typename T, int UNITS, int OPS>
+  __device__ __forceinline__ void clear(int cols) const {
+    constexpr int H = static_cast<int>(sizeof(T) / 2);
 #pragma unroll
-    for (int k = 0; k < K * PER; ++k) slots[k * threads + tid] = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < K * PER; ++k)
+      if (C::at(k / (OPS * H) % UNITS, k % H * 8 / H) >= cols) slots[k * threads + tid] = make_uint4(0, 0, 0, 0);
   }
   // unit i of a row, in sizeof(T) / 2 pieces from `piece` on
   template <typename C, typename T>
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const NormParams
   const Ring<K, R * UNITS * UP> ring(ring_smem);
   int flip = 0;
   pdl_launch_dependents();
-  if (VEC) ring.clear();
+  if constexpr (VEC && sizeof(X) == 4) ring.template clear<C, X, UNITS, 1>(p.cols);
   pdl_wait();
   const float n = static_cast<float>(p.cols);
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y * R;
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_grad_kernel(const NormP
   int flip = 0;
   float2 dg[UNITS][4] = {}, db[UNITS][4] = {}, g[UNITS][4] = {};
   pdl_launch_dependents();
-  if (VEC) ring.clear();
+  if constexpr (VEC && sizeof(X) == 4) ring.template clear<C, X, UNITS, 2>(p.cols);
   pdl_wait();
   const float n = static_cast<float>(p.cols);
   const long long step = static_cast<long long>(gridDim.x) * blockDim.y * R;
