@@ -16,7 +16,7 @@
 // the warps that add.  (Writing zeros everywhere beside the sort instead made
 // the sort, which waits for L2, four times as long.)  Measured: the lookup of
 // 32768 x 4096 in 80 us (0.89 of the copy rate); the gradient of 65536 tokens x
-// 1664 in 156 us (0.63), of which the rows take 121, short of loads in flight,
+// 1664 in 158 us (0.62), of which the rows take 121, short of loads in flight,
 // and the sort 28 (both under a profiler).
 //
 // The sort is a least-significant-digit radix sort (stable, so positions stay

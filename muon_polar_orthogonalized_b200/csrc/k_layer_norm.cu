@@ -18,8 +18,8 @@
 // a row reads it from there again.  What bounds it then is the chain of a row's
 // two sums (exchange, barrier, exchange: about 1.2 us a row for the few groups
 // an SM holds), so a group takes R rows at a time and sums all of them in one
-// exchange.  Measured: 32768 x 4096 bf16 forward in 102 us (0.81 of the copy
-// rate) and backward in 154 us (0.80), where 70% and 62% of the cycles issue an
+// exchange.  Measured: 32768 x 4096 bf16 forward in 104 us (0.79 of the copy
+// rate) and backward in 153 us (0.81), where 70% and 62% of the cycles issue an
 // instruction; 8192 x 4096 fp32 in 48 us (0.85) and 68 us (0.91).  Gain and bias stay in registers (read from L1 for every row, they
 // kept it 82% busy).  Backward, a thread keeps its columns' dgain and dbias sums
 // in registers; the block's groups are added in order into one partial row per
