@@ -552,9 +552,13 @@ static cudaError_t forward_launch(const NormParams& p, cudaStream_t s) {
 template <typename X, typename Y, bool VEC>
 static cudaError_t forward_shape(const NormParams& p, cudaStream_t s) {
   if constexpr (!VEC) {
+    // 8192 rows of 2563 and 4095 bf16: 82 and 93 us with two blocks per SM, 101
+    // and 103 with three, whose registers spill.  Above 4096, one row kept in
+    // registers or four read again, 8191 wide: fp32 195 and 212 us, bf16 253 and
+    // 199.
     if (p.cols <= 2048) return forward_launch<X, Y, false, 1, kNormThreads, 4, 1, 1, true>(p, s);
-    if (p.cols <= 4096) return forward_launch<X, Y, false, 2, kNormThreads, 3, 4, 1, true>(p, s);
-    if (p.cols <= 8192) return forward_launch<X, Y, false, 2, 512, 1, 4, 1, true>(p, s);
+    if (p.cols <= 4096) return forward_launch<X, Y, false, 2, kNormThreads, 2, 4, 1, true>(p, s);
+    if (p.cols <= 8192) return forward_launch<X, Y, false, 2, 512, 1, sizeof(X) == 2 ? 4 : 1, 1, true>(p, s);
     return forward_launch<X, Y, false, 2, 1024, 1, 2, 1, false>(p, s);
   } else {
     // One row at a time up to 8 rows per SM, several per exchange beyond (bf16,
