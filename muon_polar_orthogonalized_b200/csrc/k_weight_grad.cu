@@ -71,7 +71,7 @@ struct WgCfg {
   static constexpr int B_BYTES = CODES / 64 * WG_CHUNK;    // restored x
   static constexpr int Q_BYTES = CODES * WG_BK;            // codes
   static constexpr int STAGE = A_BYTES + B_BYTES + Q_BYTES;
-  static constexpr int STAGES = WIDE ? 4 : 7;
+  static constexpr int STAGES = WIDE ? 4 : 8;
   // a stage has WG_BK rows of CODES / 16 tasks of 16 codes, one per thread: the
   // sixteen warps form GROUPS that take the stages in turn
   static constexpr int ROW_TASKS = CODES / 16;
@@ -83,6 +83,10 @@ struct WgCfg {
   static_assert(SMEM <= 232448, "shared memory per block");
   static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(GROUPS * GROUP_WARPS == WG_WARPS && kCkptBlock % CODES == 0, "one exponent per row");
+  // A wait by parity tells a phase from the one next to it alone, so whoever
+  // waits for a slot's codes must do so at every use of the slot: each slot
+  // belongs to one group.
+  static_assert(STAGES % GROUPS == 0, "a group would miss phases of its slots");
 };
 constexpr uint32_t kTimeout = 1u;              // status word bit (muon_query_status)
 }  // namespace

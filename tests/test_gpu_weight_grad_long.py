@@ -1,0 +1,35 @@
+"""The weight gradient from an 8-bit checkpoint where a tile's row blocks go
+round the ring of stages several times, against 64-bit statements."""
+import pytest
+import torch
+
+from muon_polar_orthogonalized_b200 import _native as N
+from muon_polar_orthogonalized_b200 import api
+from tests import operator_refs as R
+from tests.test_gpu_operators import dev, wg_checkpoint, whole, ws  # noqa: F401  (dev: fixture)
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("ddt", [BF16, F32])
+@pytest.mark.parametrize("rows,n,k", [(1024, 2048, 1024), (4096, 768, 768), (2048, 1024, 1024), (1500, 1664, 768),
+                                      (1987, 500, 777), (5000, 96, 40)])
+def test_many_stages_per_tile_on_whole_numbers(dev, ddt, rows, n, k):
+    """16 to 79 row blocks a tile (three times as many for fp32 dy).  The sums
+    are whole numbers below 2^24: every stage's codes and exponents must meet
+    their own rows of dy."""
+    ck, values = wg_checkpoint(rows, k, 60, dev, "whole")
+    # powers of two that change from row to row and block to block
+    g = torch.Generator().manual_seed(61)
+    shift = torch.randint(0, 3, ck.exponents.shape, generator=g).to(torch.uint8)
+    ck.exponents += shift.to(dev)
+    values = R.checkpoint_values(ck.codes, ck.exponents, k)
+    dy = whole((rows, n), -4, 4, ddt, 62, dev)
+    want, _ = R.weight_grad(dy, values)
+    w = ws(api.muon_checkpoint_weight_grad_workspace_size(rows, n, k, ddt), dev)
+    for _ in range(3):
+        grad = torch.full((n, k), float("nan"), device=dev)
+        api.muon_checkpoint_weight_grad(dy, ck, grad, w)
+        assert torch.equal(R.f64(grad), want)
+        assert api.muon_query_status(w) == N.MUON_OK
