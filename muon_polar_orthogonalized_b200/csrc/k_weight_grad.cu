@@ -41,7 +41,11 @@
 // order.  dy in fp32, or with rows that TMA cannot read, is first staged in
 // the workspace as bf16: one plane for bf16, three for fp32 (each value is
 // the sum of its three parts to the last bit), which the product walks one
-// after another as if the rows repeated.
+// after another as if the rows repeated.  The plane of the lowest bits comes
+// first: the tensor cores cut what lies below a step of the running sum at
+// every addition, so the two lower planes are added while the sum is 2^-16 and
+// 2^-8 of what it will be (777 x 1664 x 768, error against 64 bits relative to
+// the gradient, root mean square: 2.2e-7, with the highest plane first 3.8e-6).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -265,6 +269,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer
     if (lane == 0) {
+      const int last_plane = p.kblocks / p.row_blocks - 1;
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_phase = 0;
       bool ok = true;
@@ -277,8 +282,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
             ok = false;
             break;
           }
-          const int plane = kb / p.row_blocks;
-          const int t0 = (kb - plane * p.row_blocks) * WG_BK;
+          const int pass = kb / p.row_blocks, plane = last_plane - pass;
+          const int t0 = (kb - pass * p.row_blocks) * WG_BK;
           uint8_t* sa = smem + stage * C::STAGE;
           uint8_t* sq = sa + C::A_BYTES + C::B_BYTES;
           sm100::mbar_arrive_expect_tx(&full_q[stage], C::Q_BYTES);

@@ -6,7 +6,7 @@ import torch
 from muon_polar_orthogonalized_b200 import _native as N
 from muon_polar_orthogonalized_b200 import api
 from tests import operator_refs as R
-from tests.test_gpu_operators import dev, wg_checkpoint, whole, ws  # noqa: F401  (dev: fixture)
+from tests.test_gpu_operators import dev, rand, wg_checkpoint, whole, ws  # noqa: F401  (dev: fixture)
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -33,3 +33,22 @@ def test_many_stages_per_tile_on_whole_numbers(dev, ddt, rows, n, k):
         api.muon_checkpoint_weight_grad(dy, ck, grad, w)
         assert torch.equal(R.f64(grad), want)
         assert api.muon_query_status(w) == N.MUON_OK
+
+
+@pytest.mark.parametrize("ddt", [BF16, F32])
+@pytest.mark.parametrize("rows,n,k", [(777, 1664, 768), (2000, 300, 260), (4096, 512, 512)])
+def test_error_of_long_sums(dev, ddt, rows, n, k):
+    """The tensor cores add 16 rows at a time and cut what lies below a step of
+    the running sum: half a step a time on average, at most u = 2^-24 of it.  The
+    terms' signs are random, so that the running sum after j of J groups is
+    sqrt(j / J) of the last in root mean square, 2/3 on average over j.  fp32
+    dy's lower planes are added to sums 2^-8 of it and less: 2 J u 2^-8.  The
+    result is rounded once."""
+    ck, values = wg_checkpoint(rows, k, 63, dev, "plain")
+    dy = rand((rows, n), 1.0, ddt, 64, dev)
+    want, _ = R.weight_grad(dy, values)
+    grad = torch.empty(n, k, device=dev)
+    api.muon_checkpoint_weight_grad(dy, ck, grad, ws(api.muon_checkpoint_weight_grad_workspace_size(rows, n, k, ddt), dev))
+    groups = (rows + 15) // 16
+    error = float((R.f64(grad) - want).norm() / want.norm())
+    assert error <= (2 / 3 * groups + 2 * groups * 2.0 ** -8 + 1) * R.U32
