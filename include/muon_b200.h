@@ -429,8 +429,10 @@ muon_status muon_checkpoint_unpack(const uint8_t* codes, int64_t code_pitch,
  * its input x [rows, k] and dy [rows, n]:
  *   grad[i][j] <- (grad[i][j] +) sum over t of dy[t][i] * x[t][j]
  * with x as the checkpoint holds it, on the bf16 tensor cores with fp32 sums
- * (their additions may drop the bits below a step).  No operand is rounded:
- * fp32 dy is taken in three bf16 parts, at three times the work.
+ * (an addition of 16 rows drops what lies below a step of the running sum).
+ * Restored x and bf16 dy are exact.  fp32 dy is taken in three bf16 parts, at
+ * three times the work: exact from 2^-110 on; of a smaller value the bits
+ * below bf16's smallest number, 2^-133, are dropped.
  * dy is read in place where it is bf16, its pointer 16-byte aligned and its
  * rows a multiple of 16 bytes apart and of 8 elements long; else it is copied
  * into the workspace first.  dy_aligned says whether it will be (0 asks for

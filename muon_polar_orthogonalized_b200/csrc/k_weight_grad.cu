@@ -40,8 +40,9 @@
 // sums to the workspace, and a second kernel adds the runs of such a tile in
 // order.  dy in fp32, or with rows that TMA cannot read, is first staged in
 // the workspace as bf16: one plane for bf16, three for fp32 (each value is
-// the sum of its three parts to the last bit), which the product walks one
-// after another as if the rows repeated.  The plane of the lowest bits comes
+// the sum of its three parts, but for what a value under 2^-110 has below bf16's
+// smallest number, 2^-133), which the product walks one after another as if the
+// rows repeated.  The plane of the lowest bits comes
 // first: the tensor cores cut what lies below a step of the running sum at
 // every addition, so the two lower planes are added while the sum is 2^-16 and
 // 2^-8 of what it will be (777 x 1664 x 768, error against 64 bits relative to
@@ -587,7 +588,8 @@ __global__ void __launch_bounds__(256) weight_grad_join_kernel(const __grid_cons
 
 // dy -> bf16 planes [planes][rows][pitch] (pitch a multiple of 64, zeros past
 // n).  fp32: v = p0 + p1 + p2, each the 8 leading significant bits of what is
-// left (cut, not rounded: nothing overflows, and 3 x 8 bits hold all 24);
+// left (cut, not rounded: nothing overflows, and 3 x 8 bits hold all 24 of a
+// value from 2^-110 on; below, what is under 2^-133 is dropped);
 // infinities and NaN go to plane 0 alone.
 // A lane takes 8 columns, a warp 256 of a row.
 template <typename D, int PLANES, bool VEC>

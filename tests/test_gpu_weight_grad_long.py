@@ -52,3 +52,33 @@ def test_error_of_long_sums(dev, ddt, rows, n, k):
     groups = (rows + 15) // 16
     error = float((R.f64(grad) - want).norm() / want.norm())
     assert error <= (2 / 3 * groups + 2 * groups * 2.0 ** -8 + 1) * R.U32
+
+
+def test_small_fp32_dy(dev):
+    """fp32 dy down to 2^-120: its three bf16 parts keep all that lies at or above
+    bf16's smallest number, 2^-133, and drop less than that of each value."""
+    rows, n, k = 300, 136, 200
+    ck, values = wg_checkpoint(rows, k, 65, dev, "plain")
+    g = torch.Generator().manual_seed(66)
+    dy = torch.randn(rows, n, generator=g) * torch.pow(2.0, torch.randint(-120, -100, (1, n), generator=g).float())
+    dy = dy.to(dev)
+    want, mag = R.weight_grad(dy, values)
+    dropped = 2.0 ** -133 * values.abs().sum(0)
+    grad = torch.empty(n, k, device=dev)
+    api.muon_checkpoint_weight_grad(dy, ck, grad, ws(api.muon_checkpoint_weight_grad_workspace_size(rows, n, k, F32), dev))
+    bound = dropped + (2 * rows + 8) * R.U32 * mag + R.U32 * want.abs() + 2.0 ** -149 * rows
+    assert bool(((R.f64(grad) - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("ddt", [BF16, F32])
+def test_subnormal_dy_is_kept(dev, ddt):
+    """Whole multiples of bf16's smallest number, 2^-133: the sums are fp32
+    subnormals and small normals, all exact."""
+    rows, n, k = 200, 72, 130
+    ck, values = wg_checkpoint(rows, k, 67, dev, "whole")
+    dy = (whole((rows, n), -4, 4, F32, 68, dev).double() * 2.0 ** -133).to(ddt)
+    want, _ = R.weight_grad(dy, values)
+    assert float(want.abs().max()) > 0
+    grad = torch.empty(n, k, device=dev)
+    api.muon_checkpoint_weight_grad(dy, ck, grad, ws(api.muon_checkpoint_weight_grad_workspace_size(rows, n, k, ddt), dev))
+    assert torch.equal(R.f64(grad), want)
