@@ -25,7 +25,7 @@ muon_status api_cuda_fail(cudaError_t e, const char* what);
 // The current device's SM count; fails unless it is compute capability 10.0.
 muon_status api_device(int* sms);
 cudaError_t api_timed_launch(int kind, cudaStream_t s, const std::function<cudaError_t()>& f);
-// 2-D or 3-D tiled tensor map over `base` (dims and box innermost first,
+// 2-D to 5-D tiled tensor map over `base` (dims and box innermost first,
 // strides in bytes of dims 1..); out-of-range elements load as zeros.
 muon_status api_tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, void* base,
                            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
