@@ -324,8 +324,8 @@ muon_status adamw_step_scheduled(const adamw_group* groups, int n_groups,
  * embedding tables and norm gains and biases; for the Muon parameters, hidden
  * matrices whose input was kept as an 8-bit checkpoint.  They write fp32 or
  * bf16 gradient buffers of the layout the step takes (dense row-major), either
- * overwriting them or adding to what they hold (`accumulate` != 0, one
- * rounding of old + new).  Sums are in fp32, in an order that depends on the
+ * overwriting them or adding to what they hold (`accumulate` != 0; old + new is
+ * an fp32 sum, rounded to bf16 where the buffer is).  Sums are in fp32, in an order that depends on the
  * shapes and ids alone: two calls on the same inputs give the same bits.
  *
  * Conventions above hold, and:
@@ -356,7 +356,8 @@ muon_status adamw_step_scheduled(const adamw_group* groups, int n_groups,
 /*
  * out[t] <- scale * table[ids[t]], t < n.  ids: device int32 or int64
  * (ids_bits 32 or 64).  An id outside [0, vocab) stands for no token (padding,
- * e.g. -1): its row of out is zeros.  The product is rounded once.
+ * e.g. -1): its row of out is zeros.  The product is rounded to fp32, and from
+ * there to bf16 where out is.
  */
 muon_status muon_embedding_forward(const void* table, int32_t table_dtype, int64_t vocab, int64_t dim,
                                    const void* ids, int32_t ids_bits, int64_t n, float scale,
