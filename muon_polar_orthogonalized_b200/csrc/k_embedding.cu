@@ -770,16 +770,18 @@ cudaError_t launch_embedding(const EmbedParams& p, cudaStream_t s) {
 }
 
 // Blocks of the sort's cluster: enough that a lane has few keys.  16 where the
-// GPU can place such a cluster (beyond the portable 8).
+// GPU can place such a cluster (beyond the portable 8).  Only what the GPU can
+// place is kept; the attribute that allows such clusters is set before each
+// launch, as in allow_smem.
 template <bool ONE>
 static cudaError_t sort_limit(int* limit) {
   static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(embedding_sort_kernel<ONE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   if (dev < 64 && (*limit = known[dev].load(std::memory_order_relaxed)) != 0) return cudaSuccess;
-  e = cudaFuncSetAttribute(embedding_sort_kernel<ONE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(16);
   cfg.blockDim = dim3(kSortThreads);
@@ -802,7 +804,7 @@ static cudaError_t sort_launch(const EmbedGradParams& p, unsigned nb, cudaStream
   const auto kern = embedding_sort_kernel<ONE>;
   int limit = 8;
   cudaError_t e = allow_smem(kern, kSortSmem);
-  if (e == cudaSuccess) e = sort_limit<ONE>(&limit);
+  if (e == cudaSuccess && nb > 8) e = sort_limit<ONE>(&limit);
   if (e != cudaSuccess) return e;
   if (nb > static_cast<unsigned>(limit)) {
     nb = limit;
