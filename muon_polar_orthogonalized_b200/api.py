@@ -275,9 +275,20 @@ def _adamw_groups(groups: Sequence[AdamWSpec]):
     return arr, keep
 
 
-def adamw_step(groups: Sequence[AdamWSpec], step: int, stream=None) -> None:
-    arr, keep = _adamw_groups(groups)
-    st = N.lib().adamw_step(arr, len(groups), int(step), c_void_p(_stream_handle(stream)))
+class AdamWArgs:
+    """AdamW groups (AdamWSpecs) checked and laid out for the library, for an
+    adamw_step that follows."""
+
+    def __init__(self, groups: Sequence[AdamWSpec]):
+        self.groups, self._keep = _adamw_groups(groups)
+        self._tensors = list(groups)   # the pointers' owners
+        self.count = len(groups)
+
+
+def adamw_step(groups, step: int, stream=None) -> None:
+    """One AdamW step of the groups (AdamWSpecs, or AdamWArgs)."""
+    a = groups if isinstance(groups, AdamWArgs) else AdamWArgs(groups)
+    st = N.lib().adamw_step(a.groups, a.count, int(step), c_void_p(_stream_handle(stream)))
     check(st, "adamw_step")
 
 

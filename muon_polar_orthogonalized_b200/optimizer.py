@@ -88,32 +88,48 @@ class MuonAdamW:
             out.append(dts.pop())
         return out
 
+    @staticmethod
+    def _factors(param: torch.Tensor, grad):
+        """The factors a gradient is given by, one per micro-batch; None for a tensor."""
+        if isinstance(grad, torch.Tensor):
+            return None
+        parts = list(grad) if isinstance(grad, (list, tuple)) else [grad]
+        if not parts or not all(isinstance(f, (api.LinearGrad, api.EmbeddingGrad)) for f in parts):
+            raise ValueError("a gradient is a tensor, a LinearGrad or EmbeddingGrad, or a list of these")
+        if param.dim() != 2:
+            raise ValueError(f"a gradient given by its factors is a matrix, its parameter is {tuple(param.shape)}")
+        return parts
+
     def _formed(self, param: torch.Tensor, grad, stream):
         """The gradient tensor of one parameter: `grad` itself, or, where it is
         given by its factors (api.LinearGrad, api.EmbeddingGrad, or a list of
         them, one per micro-batch), their sum, formed in param.grad (allocated
         in param.grad_dtype, else fp32, where there is none)."""
-        if grad is None or isinstance(grad, torch.Tensor):
+        parts = MuonAdamW._factors(param, grad)
+        if parts is None:
             return grad
-        parts = list(grad) if isinstance(grad, (list, tuple)) else [grad]
-        if not parts or not all(isinstance(f, (api.LinearGrad, api.EmbeddingGrad)) for f in parts):
-            raise ValueError("a gradient is a tensor, a LinearGrad or EmbeddingGrad, or a list of these")
-        # allocated on the stream that writes them, so that memory freed on
-        # another stream is not reused while it is still read there
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            if param.grad is None:
-                param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
-                                              requires_grad=False)
-            need = max(f.workspace_size(param.grad) for f in parts)
-            ws = self._factor_workspace
-            if ws is None or ws.numel() < need:
-                if ws is not None and ws.is_cuda:   # steps before this one may still be using it, on any stream
-                    ws.record_stream(torch.cuda.current_stream(ws.device))
-                ws = self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
-            if torch.cuda.is_current_stream_capturing() and not any(w is ws for w in self._captured_workspaces):
-                self._captured_workspaces.append(ws)
-        for k, f in enumerate(parts):
-            f.write(param.grad, self._factor_workspace, accumulate=k > 0, stream=stream)
+        fresh = param.grad is None
+        try:
+            # allocated on the stream that writes them, so that memory freed on
+            # another stream is not reused while it is still read there
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                if fresh:
+                    param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
+                                                  requires_grad=False)
+                need = max(f.workspace_size(param.grad) for f in parts)
+                ws = self._factor_workspace
+                if ws is None or ws.numel() < need:
+                    if ws is not None and ws.is_cuda:   # steps before this one may still be using it, on any stream
+                        ws.record_stream(torch.cuda.current_stream(ws.device))
+                    ws = self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
+                if torch.cuda.is_current_stream_capturing() and not any(w is ws for w in self._captured_workspaces):
+                    self._captured_workspaces.append(ws)
+            for k, f in enumerate(parts):
+                f.write(param.grad, self._factor_workspace, accumulate=k > 0, stream=stream)
+        except Exception:
+            if fresh:   # not a gradient: not all of it has been written
+                param.grad = None
+            raise
         return param.grad
 
     @torch.no_grad()
@@ -130,18 +146,40 @@ class MuonAdamW:
         gradient may be given by its factors (api.LinearGrad for a hidden
         matrix whose input was kept as an 8-bit checkpoint, api.EmbeddingGrad
         for an embedding table, or a list of them, one per micro-batch): the
-        step then forms it in the parameter's .grad, from nothing."""
-        self.step_count += 1
+        step then forms it in the parameter's .grad, from nothing.  A gradient
+        that is refused, in either list, is refused before any parameter or
+        state has changed (gradients formed by then stay in their .grad)."""
+        def given(params, of_call, wrong_length: str, missing: str) -> List:
+            """What stands for each parameter's gradient, lengths and types checked."""
+            if of_call is None:
+                of_call = [p.grad for p in params]
+            if len(of_call) != len(params):
+                raise ValueError(wrong_length)
+            for p, x in zip(params, of_call):
+                if x is None:
+                    raise ValueError(missing)
+                self._factors(p, x)
+            return list(of_call)
+
+        grads: List = []
         if self.muon_params:
-            if muon_grads is not None:
-                if len(muon_grads) != len(self.muon_params):
-                    raise ValueError("muon_grads must hold one gradient per Muon parameter")
-                grads = [self._formed(p, muon_grads[k], stream) for p, k in zip(self.muon_params, self._order)]
-            else:
-                grads = [p.grad for p in self.muon_params]
-            if any(g is None for g in grads):
-                raise ValueError("every Muon parameter needs a .grad")
-            gd = self._grad_dtypes(grads)
+            if muon_grads is not None and len(muon_grads) == len(self._order):
+                muon_grads = [muon_grads[k] for k in self._order]
+            grads = given(self.muon_params, muon_grads, "muon_grads must hold one gradient per Muon parameter",
+                          "every Muon parameter needs a .grad")
+        if adamw_grads is not None and len(adamw_grads) != len(self.adamw_groups):
+            raise ValueError("adamw_grads must hold one list per AdamW group")
+        grads_a = [given(g["params"], None if adamw_grads is None else adamw_grads[gi],
+                         f"adamw_grads[{gi}] must hold one gradient per parameter of its group",
+                         "every AdamW parameter needs a .grad") for gi, g in enumerate(self.adamw_groups)]
+        grads = [self._formed(p, x, stream) for p, x in zip(self.muon_params, grads)]
+        grads_a = [[self._formed(p, x, stream) for p, x in zip(g["params"], xs)]
+                   for g, xs in zip(self.adamw_groups, grads_a)]
+        gd = self._grad_dtypes(grads)
+        adamw = api.AdamWArgs([
+            api.AdamWSpec(g["params"], xs, g["exp_avg"], g["exp_avg_sq"], g["lr"], g["betas"][0], g["betas"][1],
+                          g["eps"], g["weight_decay"]) for g, xs in zip(self.adamw_groups, grads_a)])
+        if self.muon_params:
             if replicas:
                 reps = [[rep[k] for k in self._order] for rep in replicas]
                 api.muon_step_replicated(self.muon_params, grads, self.momentum, self._groups(gd), self.lr,
@@ -151,22 +189,9 @@ class MuonAdamW:
                 api.muon_step(self.muon_params, grads, self.momentum, self._groups(gd), self.lr,
                               self.beta, self.wd, self.ns_steps, self.coeffs, self.flags,
                               self.workspace, stream=stream)
-        specs = []
-        if adamw_grads is not None and len(adamw_grads) != len(self.adamw_groups):
-            raise ValueError("adamw_grads must hold one list per AdamW group")
-        for gi, g in enumerate(self.adamw_groups):
-            if adamw_grads is not None:
-                if len(adamw_grads[gi]) != len(g["params"]):
-                    raise ValueError(f"adamw_grads[{gi}] must hold one gradient per parameter of its group")
-                grads = [self._formed(p, x, stream) for p, x in zip(g["params"], adamw_grads[gi])]
-            else:
-                grads = [p.grad for p in g["params"]]
-            if any(x is None for x in grads):
-                raise ValueError("every AdamW parameter needs a .grad")
-            specs.append(api.AdamWSpec(g["params"], grads, g["exp_avg"], g["exp_avg_sq"], g["lr"],
-                                       g["betas"][0], g["betas"][1], g["eps"], g["weight_decay"]))
-        if specs:
-            api.adamw_step(specs, self.step_count, stream=stream)
+        self.step_count += 1
+        if self.adamw_groups:
+            api.adamw_step(adamw, self.step_count, stream=stream)
 
     def state_dict(self) -> dict:
         """Step count and optimizer state; "momentum" follows the order in
