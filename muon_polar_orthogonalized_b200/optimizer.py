@@ -70,8 +70,10 @@ class MuonAdamW:
         nbytes = ws_need if workspace_bytes is None else max(int(workspace_bytes), 0)
         dev = self.muon_params[0].device if self.muon_params else torch.device("cuda")
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        self.workspace[:256].zero_()   # its status word, before the first step writes it
         self._factor_workspace: Optional[torch.Tensor] = None   # grown by the gradients formed here
         self._captured_workspaces: List[torch.Tensor] = []        # those that a captured step writes when replayed
+        self._factor_status = torch.zeros(1, dtype=torch.int32, device=dev)   # their status words together
 
     def _groups(self, grad_dtypes):
         """Group descriptors, one gradient dtype per shape group."""
@@ -100,11 +102,26 @@ class MuonAdamW:
             raise ValueError(f"a gradient given by its factors is a matrix, its parameter is {tuple(param.shape)}")
         return parts
 
-    def _formed(self, param: torch.Tensor, grad, stream):
+    def _reserve(self, need: int, device) -> None:
+        """A factor workspace of at least `need` bytes, allocated on the current stream."""
+        ws = self._factor_workspace
+        if ws is None or ws.numel() < need:
+            if ws is not None and ws.is_cuda:   # steps before this one may still be using it, on any stream
+                ws.record_stream(torch.cuda.current_stream(ws.device))
+            ws = self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        if torch.cuda.is_current_stream_capturing() and not any(w is ws for w in self._captured_workspaces):
+            self._captured_workspaces.append(ws)
+
+    def _formed(self, param: torch.Tensor, grad, stream, first: int = 0):
         """The gradient tensor of one parameter: `grad` itself, or, where it is
         given by its factors (api.LinearGrad, api.EmbeddingGrad, or a list of
         them, one per micro-batch), their sum, formed in param.grad (allocated
-        in param.grad_dtype, else fp32, where there is none)."""
+        in param.grad_dtype, else fp32, where there is none).
+
+        first: factors formed before these in the same step.  Every call has its
+        status word at the start of its workspace and clears it, so factor i of
+        a step takes the workspace from 256 i on: its word, and below it those
+        of the factors before, which no later one touches."""
         parts = MuonAdamW._factors(param, grad)
         if parts is None:
             return grad
@@ -116,21 +133,47 @@ class MuonAdamW:
                 if fresh:
                     param.grad = torch.empty_like(param, dtype=getattr(param, "grad_dtype", None) or torch.float32,
                                                   requires_grad=False)
-                need = max(f.workspace_size(param.grad) for f in parts)
-                ws = self._factor_workspace
-                if ws is None or ws.numel() < need:
-                    if ws is not None and ws.is_cuda:   # steps before this one may still be using it, on any stream
-                        ws.record_stream(torch.cuda.current_stream(ws.device))
-                    ws = self._factor_workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=param.device)
-                if torch.cuda.is_current_stream_capturing() and not any(w is ws for w in self._captured_workspaces):
-                    self._captured_workspaces.append(ws)
+                MuonAdamW._reserve(self, max(256 * (first + k) + f.workspace_size(param) for k, f in enumerate(parts)),
+                                   param.device)
             for k, f in enumerate(parts):
-                f.write(param.grad, self._factor_workspace, accumulate=k > 0, stream=stream)
+                f.write(param.grad, self._factor_workspace[256 * (first + k):], accumulate=k > 0, stream=stream)
         except Exception:
             if fresh:   # not a gradient: not all of it has been written
                 param.grad = None
             raise
         return param.grad
+
+    def _form_all(self, params: Sequence[torch.Tensor], grads: Sequence, stream) -> List[torch.Tensor]:
+        """The gradient tensors of all parameters; the status words of what is
+        formed here go into _factor_status."""
+        parts = [self._factors(p, x) or [] for p, x in zip(params, grads)]
+        sizes = [f.workspace_size(p) for p, fs in zip(params, parts) for f in fs]
+        if not sizes:
+            return list(grads)
+        on_stream = lambda: torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+        with on_stream():   # the whole step's, so that no word is lost to a larger workspace halfway
+            self._reserve(max(256 * i + n for i, n in enumerate(sizes)), self._factor_status.device)
+        out, first = [], 0
+        for p, x, fs in zip(params, grads, parts):
+            out.append(self._formed(p, x, stream, first))
+            first += len(fs)
+        with on_stream():
+            words = self._factor_workspace[:256 * first].view(torch.int32).view(first, 64)[:, 0]
+            self._factor_status.bitwise_or_(words.amax())
+        return out
+
+    def query_status(self, stream=None) -> int:
+        """MUON_ERR_TIMEOUT where a bounded wait on the device ran out: in the
+        last Muon step, or, since the last call (the record is then cleared), in
+        an AdamW step on this device or in a gradient that a step formed from
+        its factors; else MUON_OK.  Synchronises `stream` (default: the current
+        one), which must be the steps' or ordered after it."""
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            formed = N.MUON_ERR_TIMEOUT if int(self._factor_status.item()) != 0 else N.MUON_OK
+            if formed != N.MUON_OK:
+                self._factor_status.zero_()
+        return next((st for st in (formed, api.muon_query_status(self.workspace, stream),
+                                   api.adamw_query_status(stream)) if st != N.MUON_OK), N.MUON_OK)
 
     @torch.no_grad()
     def step(self, stream=None, replicas: Optional[Sequence[Sequence[torch.Tensor]]] = None,
@@ -148,7 +191,8 @@ class MuonAdamW:
         for an embedding table, or a list of them, one per micro-batch): the
         step then forms it in the parameter's .grad, from nothing.  A gradient
         that is refused, in either list, is refused before any parameter or
-        state has changed (gradients formed by then stay in their .grad)."""
+        state has changed (gradients formed by then stay in their .grad).  Waits
+        on the device are bounded; query_status says whether one ran out."""
         def given(params, of_call, wrong_length: str, missing: str) -> List:
             """What stands for each parameter's gradient, lengths and types checked."""
             if of_call is None:
@@ -172,9 +216,11 @@ class MuonAdamW:
         grads_a = [given(g["params"], None if adamw_grads is None else adamw_grads[gi],
                          f"adamw_grads[{gi}] must hold one gradient per parameter of its group",
                          "every AdamW parameter needs a .grad") for gi, g in enumerate(self.adamw_groups)]
-        grads = [self._formed(p, x, stream) for p, x in zip(self.muon_params, grads)]
-        grads_a = [[self._formed(p, x, stream) for p, x in zip(g["params"], xs)]
-                   for g, xs in zip(self.adamw_groups, grads_a)]
+        formed = self._form_all(self.muon_params + [p for g in self.adamw_groups for p in g["params"]],
+                                grads + [x for xs in grads_a for x in xs], stream)
+        grads, at = formed[:len(grads)], len(grads)
+        for gi, xs in enumerate(grads_a):
+            grads_a[gi], at = formed[at:at + len(xs)], at + len(xs)
         gd = self._grad_dtypes(grads)
         adamw = api.AdamWArgs([
             api.AdamWSpec(g["params"], xs, g["exp_avg"], g["exp_avg_sq"], g["lr"], g["betas"][0], g["betas"][1],

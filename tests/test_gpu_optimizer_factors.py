@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from muon_polar_orthogonalized_b200 import _native as N
 from muon_polar_orthogonalized_b200 import api
 from muon_polar_orthogonalized_b200.optimizer import MuonAdamW
 from tests.test_gpu_operators import dev, token_ids  # noqa: F401  (dev: fixture)
@@ -52,3 +53,52 @@ def test_a_refused_step_changes_nothing_and_may_be_made_again(dev):
     fresh.step(**factors(c))
     assert opt.step_count == fresh.step_count == 1
     assert all(torch.equal(x, y) for x, y in zip(state(b, opt), state(c, fresh)))
+
+
+class TimedOut(api.LinearGrad):
+    """A factor in whose call a bounded wait runs out (the library's own test of
+    its waits, on the call's workspace; the gradient is written as usual)."""
+
+    def write(self, grad, workspace, accumulate=False, stream=None):
+        super().write(grad, workspace, accumulate=accumulate, stream=stream)
+        s = torch.cuda.current_stream(grad.device) if stream is None else stream
+        assert N.lib().muon_selftest_wait_timeout(workspace.data_ptr(), 1000000, s.cuda_stream) == N.MUON_OK
+
+
+@pytest.mark.parametrize("place", [0, 1, 2])
+def test_a_timeout_in_a_factor_is_reported(dev, place):
+    b, opt = made(dev)
+    assert opt.query_status() == N.MUON_OK
+    good = factors(b)
+    opt.step(**good)
+    assert opt.query_status() == N.MUON_OK
+    parts = [api.LinearGrad(b.dy, b.ckpt) for _ in range(3)]
+    parts[place] = TimedOut(b.dy, b.ckpt)
+    opt.step(**dict(good, muon_grads=[parts]))
+    opt.step(**good)
+    assert opt.query_status() == N.MUON_ERR_TIMEOUT
+    assert opt.query_status() == N.MUON_OK
+
+
+def test_a_timeout_in_a_replayed_step_is_reported(dev):
+    """On a stream of its own, captured, and the workspace outgrown since."""
+    b, opt = made(dev)
+    big = Block(dev, tokens=6000, seed=7)
+    big.forward()
+    big.backward_norm()
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    opt.step(stream=side, **factors(b))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        opt.step(stream=side, **dict(factors(b), muon_grads=[TimedOut(b.dy, b.ckpt)]))
+    assert opt.query_status(side) == N.MUON_OK
+    opt.step(stream=side, **factors(big))
+    assert opt.query_status(side) == N.MUON_OK
+    with torch.cuda.stream(side):
+        graph.replay()
+    opt.step(stream=side, **factors(big))
+    assert opt.query_status(side) == N.MUON_ERR_TIMEOUT
+    assert opt.query_status(side) == N.MUON_OK
+    del graph

@@ -36,6 +36,7 @@ def opt(monkeypatch):
     o.step_count = 0
     o.workspace = torch.zeros(256, dtype=torch.uint8)
     o._factor_workspace, o._captured_workspaces = None, []
+    o._factor_status = torch.zeros(1, dtype=torch.int32)
     o.launched = []
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     for name in ("muon_step", "muon_step_replicated"):
@@ -79,3 +80,44 @@ def test_a_gradient_that_was_not_formed_is_not_left_behind(opt):
     with pytest.raises(ValueError, match="another shape"):
         opt.step(muon_grads=MG(), adamw_grads=[[Factor(fails=True), AG()[1]]])
     assert p.grad is kept
+
+
+class Reporting(Factor):
+    """A factor whose call clears its status word, fills its scratch, and reports."""
+
+    def __init__(self, word, need):
+        self.fails, self.word, self.need = False, word, need
+
+    def workspace_size(self, grad):
+        return self.need
+
+    def write(self, grad, workspace, accumulate=False, stream=None):
+        assert workspace.data_ptr() % 4 == 0 and workspace.numel() >= self.need
+        workspace[:self.need] = 0x5A
+        workspace[:4].view(torch.int32)[0] = self.word
+        grad.fill_(1.0)
+
+
+def test_a_factor_that_reports_is_not_forgotten(opt, monkeypatch):
+    """The word of any factor of a step reaches query_status, whatever the later
+    factors and steps write, and once."""
+    from muon_polar_orthogonalized_b200 import _native as N
+    muon, adamw = [N.MUON_OK], [N.MUON_OK]
+    monkeypatch.setattr(api, "muon_query_status", lambda ws, stream=None: muon[0])
+    monkeypatch.setattr(api, "adamw_query_status", lambda stream=None: adamw[0])
+    opt.adamw_groups = []
+    assert opt.query_status() == N.MUON_OK
+    for k in range(4):
+        words = [Reporting(1 if i == k else 0, need) for i, need in enumerate((300, 5000, 256, 100000 >> k))]
+        opt.step(muon_grads=[words[:3], words[3]])
+        opt.step(muon_grads=[Reporting(0, 700), [Reporting(0, 256), Reporting(0, 256)]])
+        opt.step(muon_grads=MG())
+        assert opt.query_status() == N.MUON_ERR_TIMEOUT
+        assert opt.query_status() == N.MUON_OK
+    opt.step(muon_grads=[Reporting(0, 300), Reporting(0, 9000)])
+    assert opt.query_status() == N.MUON_OK
+    muon[0] = N.MUON_ERR_TIMEOUT
+    assert opt.query_status() == N.MUON_ERR_TIMEOUT
+    muon[0], adamw[0] = N.MUON_OK, N.MUON_ERR_TIMEOUT
+    assert opt.query_status() == N.MUON_ERR_TIMEOUT
+    assert len(opt.launched) == 13
