@@ -319,6 +319,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) weight_grad_tc_kernel(const __g
                  sm100::globaltimer() - t < 100000000ull) {
           }
         }
+        // the second CTA's dy signals the leader's barriers, which it cannot wait
+        // on, in phases that the leader may not have begun: a load takes
+        // microseconds, so a millisecond stands for its landing
+        const uint64_t t = sm100::globaltimer();
+        while (rank != 0 && sm100::globaltimer() - t < 1000000ull) {
+        }
       }
     }
   } else if (warp == 1) {
