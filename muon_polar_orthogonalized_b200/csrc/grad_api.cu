@@ -133,7 +133,9 @@ struct WeightWs {
 };
 // The plan for one tile geometry.
 WeightWs weight_plan(WeightWs w, int wide, int64_t n, int64_t k) {
-  constexpr int kPairs = 74;   // CTA pairs of the GPU (148 SMs)
+  // CTA pairs of a B200 (148 SMs).  A workspace is sized without a device, so the
+  // count is fixed; with fewer SMs pairs only queue, since none waits for another.
+  constexpr int kPairs = 74;
   const WgCost& c = kWgCost[wide];
   w.wide = wide;
   w.tiles_n = (n + kWgTile[wide].n - 1) / kWgTile[wide].n;

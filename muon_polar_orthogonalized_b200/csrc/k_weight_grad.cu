@@ -20,12 +20,13 @@
 // 256x256x16 MMAs, two per 16 rows (one for each half of the dy columns), into
 // one 512-column accumulator: restored codes are used for 512 columns of dy,
 // which leaves the sixteen warps 1024 tensor-pipe cycles per stage.  The same
-// sixteen warps write the finished tile.  Measured: 1.53 PFLOP/s at 16384 x
-// 14336 x 4096 (1.26 ms, 1.13 of the measured sustained bf16 product, 0.95 of
-// its burst; 1.30 in a long loop, at the power cap), 1.32 at 16384 x 1024 x 4096.  Where there are few tiles, or few
+// sixteen warps write the finished tile.  Measured on two boards: 1.48 to 1.53
+// PFLOP/s at 16384 x 14336 x 4096 (1.26 to 1.30 ms, 1.09 to 1.13 of the measured
+// sustained bf16 product; 1.29 in a long loop, at the power cap), 1.20 to 1.32
+// at 16384 x 1024 x 4096.  Where there are few tiles, or few
 // rows, a tile's start and drain (11 us) outweigh its product, and tiles of
 // 256 by 128 are used, on which two groups of eight warps take the stages in
-// turn: 11.4 us against 19.3 at 777 x 1664 x 768 and 16.3 against 22.2 at 4096 x
+// turn: 11.5 us against 19.3 at 777 x 1664 x 768 and 16.2 against 22.2 at 4096 x
 // 768 x 768, but 139 against 98 at 16384 x 1664 x 1664 and 0.74 PFLOP/s at
 // 16384 x 14336 x 4096.  The choice is by the estimated time (grad_api.cu).
 //   warp 0: TMA producer   warp 1: MMA issuer (+ TMEM owner)
