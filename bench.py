@@ -56,8 +56,8 @@ FALLBACK_PEAKS = {"hbm_gbs": 6650.0, "bf16_tflops": 1590.0, "bf16_tflops_sustain
 # the 8B shapes and scaled x32 (the slice is exactly 1/32 of the set: same
 # seven shapes, 1 layer instead of 32).
 TRAFFIC_CAPTURES = {
-    "ns_axpy": {"sources": ["k_gemm_tc.cu", "sm100.cuh", "common.cuh", "muon_api.cu"], "sha": "253ab92629fdb298",
-                "bytes_per_pass": {"llama_8b_32l": 32 * 990843392, "llama_8b_1layer": 990843392}},
+    "ns_axpy": {"sources": ["k_gemm_tc.cu", "sm100.cuh", "common.cuh", "muon_api.cu"], "sha": "1b80b285fe198c95",
+                "bytes_per_pass": {"llama_8b_32l": 32 * 1005381376, "llama_8b_1layer": 1005381376}},
 }
 
 
