@@ -146,10 +146,10 @@ class MuonAdamW:
     def _form_all(self, params: Sequence[torch.Tensor], grads: Sequence, stream) -> List[torch.Tensor]:
         """The gradient tensors of all parameters; the status words of what is
         formed here go into _factor_status."""
+        if all(isinstance(x, torch.Tensor) for x in grads):
+            return list(grads)
         parts = [self._factors(p, x) or [] for p, x in zip(params, grads)]
         sizes = [f.workspace_size(p) for p, fs in zip(params, parts) for f in fs]
-        if not sizes:
-            return list(grads)
         on_stream = lambda: torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
         with on_stream():   # the whole step's, so that no word is lost to a larger workspace halfway
             self._reserve(max(256 * i + n for i, n in enumerate(sizes)), self._factor_status.device)
@@ -202,7 +202,8 @@ class MuonAdamW:
             for p, x in zip(params, of_call):
                 if x is None:
                     raise ValueError(missing)
-                self._factors(p, x)
+                if not isinstance(x, torch.Tensor):
+                    self._factors(p, x)
             return list(of_call)
 
         grads: List = []
